@@ -148,6 +148,9 @@ def prepare(case, seed):
     if case["op"] == "plan":
         s["ids"] = _route(case, g).to(torch.int64 if case["ids"] == "i64" else torch.int32).contiguous()
         P = case["n"] * case["topk"]
+        if own:
+            import rank_augmented_quantized_amd as tq
+            s["ws"] = tq.expert_plan_workspace(case["n"], case["topk"], case["E"], "cuda")
         s["out"] = (torch.zeros(case["E"] + 1, dtype=torch.int32, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda"),
                     torch.zeros((case["n"], case["topk"]), dtype=torch.int32, device="cuda"))
     elif case["op"] == "combine":
@@ -293,7 +296,7 @@ def _own(s):
     case = s["case"]
     if case["op"] == "plan":
         offsets, order, pos = s["out"]
-        return tq.tq_expert_plan(s["ids"], case["E"], offsets=offsets, order=order, pos=pos)
+        return tq.tq_expert_plan(s["ids"], case["E"], offsets=offsets, order=order, pos=pos, ws=s["ws"])
     if case["op"] == "combine":
         return tq.tq_expert_combine(s["Z"], s["pos"], s["weights"], residual=s["res"], Y=s["Y"])
     if case["op"] == "act":
