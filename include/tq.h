@@ -68,10 +68,16 @@ typedef enum {
   TQ_ERR_BITS = -4,      /* unsupported bit width */
   TQ_ERR_ALIGN = -5,     /* a pointer is not 16-byte aligned */
   TQ_ERR_WORKSPACE = -6, /* workspace smaller than the queried size */
-  TQ_ERR_HIP = -7        /* the HIP runtime reported an error */
+  TQ_ERR_HIP = -7,       /* the HIP runtime reported an error */
+  TQ_ERR_ACT = -8        /* unknown activation */
 } tq_status;
 
 typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
+
+/* Activations of tq_linear_act and tq_linear_experts: x, max(x, 0),
+ * x sigmoid(x), x Phi(x) (error function), and
+ * x sigmoid(2 sqrt(2 / pi) (x + 0.044715 x^3)) (the tanh form of GELU). */
+typedef enum { TQ_ACT_NONE = 0, TQ_ACT_RELU = 1, TQ_ACT_SILU = 2, TQ_ACT_GELU = 3, TQ_ACT_GELU_TANH = 4 } tq_act;
 
 /* Human-readable name of a status (static string, never NULL). */
 const char* tq_status_string(tq_status s);
@@ -446,6 +452,104 @@ tq_status tq_linear_qlr(const void* X, tq_dtype x_dt, int64_t n, int64_t d, int6
  * the ranks).  For tests.
  */
 tq_status tq_linear_qlr_workspace_offsets(int64_t n, int64_t d, int64_t r, size_t off[4]);
+
+/*
+ * tq_linear_act -- the rank-augmented layer with what follows it in its
+ * epilogue (TwinQuant notes, section 04.C: both components meet in one
+ * epilogue with one store of Y):
+ *
+ *   v = s_x s_w^T (.) (C_x C_w^T) + (X L1) L2 + bias
+ *   Y = act(v) + residual                                        (gated == 0)
+ *   Y[:, j] = act(v[:, j]) v[:, m / 2 + j] + residual[:, j]      (gated != 0)
+ *
+ *   X, n, d, m, r, w_codes, s_w, lowrank   as tq_linear; m counts the weight's
+ *            channels.  A gated layer (gate and up projection of one input)
+ *            is one weight of m channels, the gate's m / 2 first, then the
+ *            up projection's, with one pair of low-rank factors; m even.
+ *   bias     m fp32, or NULL.
+ *   residual n x mo (res_dt), mo = m / 2 when gated, else m; or NULL.  It may
+ *            be Y itself (same type).  Otherwise no input overlaps Y.
+ *   Y        out: n x mo (y_dt), rounded once from the fp32 epilogue.
+ *   ws       tq_linear_act_workspace_bytes(n, d, m, r) bytes, zero-filled once
+ *            before its first use (as tq_linear's); calls that share it must
+ *            be ordered.
+ * Codes, scales and integer sums are tq_linear's.  T = X L1 enters the second
+ * low-rank stage as two (bf16 Y) or three (fp32 Y) bf16 parts, within 2^-16 or
+ * 2^-24 of its fp32 sum, so that Y's own type decides its accuracy.  Errors as tq_linear, plus TQ_ERR_ACT, and
+ * TQ_ERR_SHAPE for a gated layer of odd m.
+ */
+size_t tq_linear_act_workspace_bytes(int64_t n, int64_t d, int64_t m, int64_t r);
+tq_status tq_linear_act(const void* X, tq_dtype x_dt, int64_t n, int64_t d, int64_t m, int64_t r,
+                        const void* w_codes, const float* s_w, const void* lowrank, const float* bias, tq_act act,
+                        int gated, const void* residual, tq_dtype res_dt, void* Y, tq_dtype y_dt, void* ws,
+                        size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Layers of a mixture of experts: E layers of one shape, each token taking
+ * topk of them.  A pair is (token t, choice j), numbered t topk + j.
+ *
+ * tq_expert_plan -- sorts the pairs by expert, on the device.
+ *   ids      n x topk expert indices, row-major, ids_bits = 32 or 64 bits
+ *            each; a pair whose id lies outside 0 .. E - 1 is dropped (a
+ *            padding token, or an expert held elsewhere).
+ *   offsets  out: E + 1 int32; the kept pairs of expert e take the sorted
+ *            positions offsets[e] .. offsets[e + 1] - 1, in pair order.
+ *   order    out: n topk int32; order[p] = pair at sorted position p.  Entries
+ *            from offsets[E] on are left as they were.
+ *   pos      out: n topk int32; sorted position of each pair, -1 if dropped.
+ *   ws       tq_expert_plan_workspace_bytes(n, topk, E) bytes of scratch (0
+ *            for small plans: ws may then be NULL).
+ * The result depends on the ids alone (no atomics decide an order).  Shapes:
+ * 1 <= E <= 1024, 1 <= topk <= 64, n topk <= 2^24; n == 0 writes offsets = 0.
+ * TQ_ERR_BITS for other id widths.
+ */
+size_t tq_expert_plan_workspace_bytes(int64_t n, int64_t topk, int64_t E);
+tq_status tq_expert_plan(const void* ids, int ids_bits, int64_t n, int64_t topk, int64_t E, int32_t* offsets,
+                         int32_t* order, int32_t* pos, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * tq_linear_experts -- tq_linear_act (without residual) on sorted rows: row p
+ * of expert e, offsets[e] <= p < offsets[e + 1], is expert e's layer on
+ * token order[p] / topk of X, or, with order NULL (then topk == 1), on row p
+ * of X (the next layer of the same experts, whose input is already sorted).
+ *   X        n x d (x_dt); n topk rows of Y.  Each token is quantised once,
+ *            whatever the number of its experts.
+ *   w_codes, s_w, bias   the E layers' stacked: E m rows of d / 2 bytes, E m
+ *            fp32, E m fp32 (or NULL).
+ *   lowrank  E blobs of tq_lowrank_bytes(d, m, r) bytes, one behind the other,
+ *            each from tq_pack_lowrank; or NULL iff r == 0.
+ *   offsets, order   from tq_expert_plan, on the device; the call never waits
+ *            for them on the host.  Offsets outside 0 .. n topk and orders
+ *            outside the pairs are clamped (no access leaves the buffers).
+ *   Y        out: n topk x mo (y_dt).  Rows from offsets[E] on are left as
+ *            they were.
+ *   ws       tq_linear_experts_workspace_bytes(n, topk, d, m, r, E) bytes,
+ *            zero-filled once before its first use; calls that share it must
+ *            be ordered.
+ * Shapes as tq_linear_act and tq_expert_plan, with n topk <= 2^24 and
+ * n d < 2^31.  Errors as tq_linear_act.
+ */
+size_t tq_linear_experts_workspace_bytes(int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E);
+tq_status tq_linear_experts(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r,
+                            int64_t E, const int32_t* offsets, const int32_t* order, const void* w_codes,
+                            const float* s_w, const void* lowrank, const float* bias, tq_act act, int gated, void* Y,
+                            tq_dtype y_dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * tq_expert_combine -- sums each token's expert outputs:
+ *   Y[t] = residual[t] + sum_j weights[t][j] Z[pos[t][j]], in order of j in
+ *   fp32, rounded once.
+ *   Z        rows x m (z_dt), sorted rows; pos n x topk from tq_expert_plan.
+ *            A pair whose pos lies outside 0 .. rows - 1 adds nothing,
+ *            whatever its weight.
+ *   weights  n x topk (w_dt).
+ *   residual n x m (res_dt) or NULL; it may be Y itself (same type).
+ *   Y        out: n x m (y_dt).
+ * 1 <= topk <= 64, 1 <= m <= 2^22; rows <= 2^24 (may be 0).
+ */
+tq_status tq_expert_combine(const void* Z, tq_dtype z_dt, int64_t rows, int64_t n, int64_t topk, int64_t m,
+                            const int32_t* pos, const void* weights, tq_dtype w_dt, const void* residual,
+                            tq_dtype res_dt, void* Y, tq_dtype y_dt, hipStream_t stream);
 
 /*
  * tq_debug_accumulate -- exact integer product of two code matrices, exported.

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/tq.h"
+#include "tq_act.h"
 #include "tq_prologue.h"
 
 namespace {
@@ -264,6 +265,7 @@ const char* tq_status_string(tq_status s) {
     case TQ_ERR_ALIGN: return "TQ_ERR_ALIGN: pointer not 16-byte aligned";
     case TQ_ERR_WORKSPACE: return "TQ_ERR_WORKSPACE: workspace too small";
     case TQ_ERR_HIP: return "TQ_ERR_HIP: HIP runtime error";
+    case TQ_ERR_ACT: return "TQ_ERR_ACT: unknown activation";
   }
   return "unknown tq_status";
 }
@@ -1159,6 +1161,175 @@ tq_status qlr_run(const void* X, tq_dtype x_dt, int64_t n, int64_t d, int64_t m,
 }
 
 }  // namespace
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// The layer with its epilogue, and experts' layers on sorted rows
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxPairs = (int64_t)1 << 24;
+constexpr int64_t kMaxTopk = 64;
+
+// Workspace of tq_linear_act (E = 0) and tq_linear_experts: the hand-off and
+// counter regions at the fixed offsets of tq_linear's, then per token its
+// scale and codes, per row the partials of T.
+struct ActWs {
+  size_t sx, xc, p, total;
+  int r_pad;
+  tq::ExpertTPlan tplan;
+};
+ActWs act_ws(int64_t n, int64_t topk, int64_t d, int64_t r, int64_t E) {
+  ActWs w{};
+  const int64_t P = n * topk;
+  w.r_pad = (int)r_padded(r);
+  size_t psize = 0;
+  if (w.r_pad > 0 && P > 0) {
+    w.tplan = tq::plan_expert_t(P, (int)E, (int)d, w.r_pad, true);
+    psize = (size_t)w.tplan.nchunk * (size_t)P * (size_t)w.r_pad * 4;
+  }
+  size_t o = tq::kSyncBytes + kCtrBytes;
+  w.sx = o;
+  o = align256(o + (size_t)n * 4);
+  w.xc = o;
+  o = align256(o + (size_t)n * (size_t)(d / 2));
+  w.p = o;
+  o = align256(o + psize);
+  w.total = o;
+  return w;
+}
+
+bool act_shape_ok(int64_t n, int64_t d, int64_t m, int64_t r) {
+  return n >= 0 && n <= kMaxDim && d > 0 && d <= kMaxK && m > 0 && m <= kMaxDim && d % 32 == 0 && r >= 0 && r <= 256;
+}
+bool experts_shape_ok(int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E) {
+  return act_shape_ok(n, d, m, r) && topk >= 1 && topk <= kMaxTopk && E >= 1 && E <= tq::kMaxExperts &&
+         n <= kMaxPairs / topk && n * d < ((int64_t)1 << 31) && E * m <= kMaxDim;
+}
+bool valid_act(tq_act a) { return a >= TQ_ACT_NONE && a <= TQ_ACT_GELU_TANH; }
+
+tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E,
+                  const int32_t* offsets, const int32_t* order, const void* w_codes, const float* s_w,
+                  const void* lowrank, const float* bias, tq_act act, int gated, const void* residual,
+                  tq_dtype res_dt, void* Y, tq_dtype y_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const ActWs L = act_ws(n, topk, d, r, E);
+  if (ws_bytes < L.total) return TQ_ERR_WORKSPACE;
+  uint8_t* base = (uint8_t*)ws;
+  const bool xb = x_dt == TQ_BF16, ex = E > 0;
+  tq::ActArgs a{};
+  a.A = base + L.xc;
+  a.sx = (const float*)(base + L.sx);
+  a.B = (const uint8_t*)w_codes;
+  a.sw = s_w;
+  a.lda = a.ldb = d / 2;
+  a.M = (int)(n * topk);
+  a.N = (int)m;
+  a.Kb = (int)(d / 2);
+  a.lowrank = (const uint8_t*)lowrank;
+  a.lr_stride = (int64_t)tq_lowrank_bytes(d, m, r);
+  a.l2_off = (int64_t)L.r_pad * d * 2;
+  a.r_pad = L.r_pad;
+  a.tparts = y_dt == TQ_F32 ? 3 : 2;
+  a.Tp = (const float*)(base + L.p);
+  a.nchunk = L.tplan.nchunk;
+  a.bias = bias;
+  a.res = residual;
+  a.res_bf16 = res_dt == TQ_BF16;
+  a.act = (int)act;
+  a.Y = Y;
+  a.y_bf16 = y_dt == TQ_BF16;
+  a.seg = tq::Segments{offsets, order, (int)E, (int)(n * topk), (int)topk, (int)n};
+  TQ_RUN("quant_rows", stream,
+         tq::launch_quant_rows_fast(X, xb, (int)n, (int)d, (int)d, 4, 4, base + L.xc, (float*)(base + L.sx), nullptr,
+                                    nullptr, stream));
+  if (L.r_pad)
+    TQ_RUN("lowrank_t", stream,
+           tq::launch_expert_t(X, xb, (int)d, a.lowrank, a.lr_stride, L.r_pad, a.seg, ex, L.tplan,
+                               (float*)(base + L.p), nullptr, a.tparts, stream));
+  TQ_RUN(ex ? "experts_rows" : "act_rows", stream, tq::launch_rows_act(a, gated != 0, ex, stream));
+  return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tq_linear_act_workspace_bytes(int64_t n, int64_t d, int64_t m, int64_t r) {
+  return act_shape_ok(n, d, m, r) ? act_ws(n, 1, d, r, 0).total : 0;
+}
+
+tq_status tq_linear_act(const void* X, tq_dtype x_dt, int64_t n, int64_t d, int64_t m, int64_t r, const void* w_codes,
+                        const float* s_w, const void* lowrank, const float* bias, tq_act act, int gated,
+                        const void* residual, tq_dtype res_dt, void* Y, tq_dtype y_dt, void* ws, size_t ws_bytes,
+                        hipStream_t stream) {
+  if (!valid_act(act)) return TQ_ERR_ACT;
+  if (residual && !valid_dtype(res_dt)) return TQ_ERR_DTYPE;
+  if (gated && m % 2) return TQ_ERR_SHAPE;
+  const tq_status st = linear_check(X, x_dt, n, d, m, r, w_codes, s_w, lowrank, Y, y_dt, ws);
+  if (st != TQ_OK || n == 0) return st;
+  if ((bias && !aligned16(bias)) || (residual && !aligned16(residual))) return TQ_ERR_ALIGN;
+  return act_run(X, x_dt, n, 1, d, m, r, 0, nullptr, nullptr, w_codes, s_w, lowrank, bias, act, gated, residual,
+                 res_dt, Y, y_dt, ws, ws_bytes, stream);
+}
+
+size_t tq_expert_plan_workspace_bytes(int64_t n, int64_t topk, int64_t E) {
+  if (n < 0 || topk < 1 || topk > kMaxTopk || E < 1 || E > tq::kMaxExperts || n > kMaxPairs / topk) return 0;
+  return tq::expert_plan_ws_bytes(n * topk, (int)E);
+}
+
+tq_status tq_expert_plan(const void* ids, int ids_bits, int64_t n, int64_t topk, int64_t E, int32_t* offsets,
+                         int32_t* order, int32_t* pos, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (ids_bits != 32 && ids_bits != 64) return TQ_ERR_BITS;
+  if (n < 0 || topk < 1 || topk > kMaxTopk || E < 1 || E > tq::kMaxExperts || n > kMaxPairs / topk)
+    return TQ_ERR_SHAPE;
+  const size_t need = tq::expert_plan_ws_bytes(n * topk, (int)E);
+  if (!offsets || (n > 0 && (!ids || !order || !pos)) || (need > 0 && !ws)) return TQ_ERR_NULL;
+  if (!aligned16(offsets) || !aligned16(ids) || !aligned16(order) || !aligned16(pos) || !aligned16(ws))
+    return TQ_ERR_ALIGN;
+  if (ws_bytes < need) return TQ_ERR_WORKSPACE;
+  TQ_RUN("expert_plan", stream,
+         tq::launch_expert_plan(ids, ids_bits == 64, n * topk, (int)E, offsets, order, pos, ws, stream));
+  return TQ_OK;
+}
+
+size_t tq_linear_experts_workspace_bytes(int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E) {
+  return experts_shape_ok(n, topk, d, m, r, E) ? act_ws(n, topk, d, r, E).total : 0;
+}
+
+tq_status tq_linear_experts(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r,
+                            int64_t E, const int32_t* offsets, const int32_t* order, const void* w_codes,
+                            const float* s_w, const void* lowrank, const float* bias, tq_act act, int gated, void* Y,
+                            tq_dtype y_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!valid_act(act)) return TQ_ERR_ACT;
+  if ((gated && m % 2) || (!order && topk != 1)) return TQ_ERR_SHAPE;
+  const tq_status st = linear_check(X, x_dt, n, d, m, r, w_codes, s_w, lowrank, Y, y_dt, ws);
+  if (st != TQ_OK) return st;
+  if (!experts_shape_ok(n, topk, d, m, r, E)) return TQ_ERR_SHAPE;
+  if (n == 0) return TQ_OK;
+  if (!offsets) return TQ_ERR_NULL;
+  if (!aligned16(offsets) || !aligned16(order) || !aligned16(bias)) return TQ_ERR_ALIGN;
+  return act_run(X, x_dt, n, topk, d, m, r, E, offsets, order, w_codes, s_w, lowrank, bias, act, gated, nullptr,
+                 TQ_BF16, Y, y_dt, ws, ws_bytes, stream);
+}
+
+tq_status tq_expert_combine(const void* Z, tq_dtype z_dt, int64_t rows, int64_t n, int64_t topk, int64_t m,
+                            const int32_t* pos, const void* weights, tq_dtype w_dt, const void* residual,
+                            tq_dtype res_dt, void* Y, tq_dtype y_dt, hipStream_t stream) {
+  if (!valid_dtype(z_dt) || !valid_dtype(w_dt) || !valid_dtype(y_dt) || (residual && !valid_dtype(res_dt)))
+    return TQ_ERR_DTYPE;
+  if (rows < 0 || rows > kMaxPairs || n < 0 || topk < 1 || topk > kMaxTopk || n > kMaxPairs / topk || m < 1 ||
+      m > ((int64_t)1 << 22))
+    return TQ_ERR_SHAPE;
+  if (n == 0) return TQ_OK;
+  if ((rows > 0 && !Z) || !pos || !weights || !Y) return TQ_ERR_NULL;
+  if (!aligned16(Z) || !aligned16(pos) || !aligned16(weights) || !aligned16(residual) || !aligned16(Y))
+    return TQ_ERR_ALIGN;
+  TQ_RUN("expert_combine", stream,
+         tq::launch_expert_combine(Z, z_dt == TQ_BF16, (int)n, (int)topk, (int)m, rows, pos, weights, w_dt == TQ_BF16,
+                                   residual, res_dt == TQ_BF16, Y, y_dt == TQ_BF16, stream));
+  return TQ_OK;
+}
+
+}  // extern "C"
 
 extern "C" {
 

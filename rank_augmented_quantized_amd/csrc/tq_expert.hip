@@ -1,0 +1,397 @@
+// Kernels around the experts' products (gfx950): the routing plan (pairs
+// sorted by expert), the first low-rank stage of the sorted rows and the
+// weighted combination of the experts' outputs.
+
+#include "tq_act.h"
+
+namespace tq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Routing plan: a stable counting sort of P = n topk pairs by expert id.
+//   offsets[e] = number of kept pairs with an expert below e, and a pair's
+//   position = offsets[its expert] + its rank among the pairs of that expert
+//   in pair order.  Pairs whose id lies outside 0 .. E - 1 are dropped.
+// Ranks come from counts alone, never from the order in which atomics land,
+// so the plan is the same on every run.  A wave ranks 64 consecutive pairs by
+// ballots over the id's bits (lanes with an equal id); its counts per expert
+// in LDS carry the rank across its rounds, and sums over the waves in wave
+// order carry it across the block.
+// A block of 16 waves takes kPlanChunk pairs.  Up to kPlanOne pairs the
+// whole plan is one block and one launch; more take two launches: the blocks'
+// histograms, then each block sums the histograms of the blocks before it.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanChunk = 2048;
+constexpr int kPlanOne = 8192;
+
+// id of pair i as an expert index, or E when dropped
+template <typename I>
+__device__ __forceinline__ int plan_id(const I* ids, int64_t i, int64_t P, int E) {
+  if (i >= P) return E;
+  const I v = ids[i];
+  return (v >= 0 && v < (I)E) ? (int)v : E;
+}
+
+// lanes of the wave with the same id (0 .. E) as this lane
+__device__ __forceinline__ uint64_t same_id(int id, int bits) {
+  uint64_t m = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (id >> b) & 1;
+    const uint64_t s = __ballot(on);
+    m &= on ? s : ~s;
+  }
+  return m;
+}
+
+// orders a wave's LDS accesses on either side, across its lanes
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <typename I>
+__global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const I* ids, int64_t P, int E, int32_t* hist) {
+  __shared__ int cnt[kMaxExperts + 1];
+  for (int e = threadIdx.x; e <= E; e += kPlanThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * kPlanChunk;
+  for (int j = threadIdx.x; j < kPlanChunk; j += kPlanThreads) atomicAdd(&cnt[plan_id(ids, i0 + j, P, E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) hist[(size_t)blockIdx.x * E + e] = cnt[e];
+}
+
+template <typename I, bool ONE>
+__global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, int E, int bits, const int32_t* hist,
+                                                       int32_t* offsets, int32_t* order, int32_t* pos) {
+  extern __shared__ int cnt[];  // [waves][E + 1]: counts, then next positions
+  __shared__ int wsum[kPlanWaves];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int stride = E + 1;
+  for (int i = tid; i < kPlanWaves * stride; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
+  // this wave's consecutive pairs
+  const int64_t b0 = ONE ? 0 : (int64_t)blockIdx.x * kPlanChunk;
+  const int64_t blen = ONE ? P : min((int64_t)kPlanChunk, P - b0);
+  const int rounds = (int)((blen + kPlanThreads - 1) / kPlanThreads);
+  const int64_t i0 = b0 + (int64_t)w * rounds * 64;
+  const int64_t iend = b0 + blen;
+  int* my = cnt + w * stride;
+  for (int r = 0; r < rounds; ++r) {
+    const int id = plan_id(ids, i0 + 64 * r + lane, iend, E);
+    const uint64_t m = same_id(id, bits);
+    if ((m & ((1ull << lane) - 1)) == 0) my[id] += __popcll(m);  // one lane per id
+    wave_sync();
+  }
+  __syncthreads();
+  // thread e: expert e's pairs in this block's waves, in all blocks, and before this block
+  int total = 0, before = 0;
+  if (tid < E) {
+    if (ONE) {
+      for (int v = 0; v < kPlanWaves; ++v) total += cnt[v * stride + tid];
+    } else {
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int h = hist[(size_t)b * E + tid];
+        total += h;
+        before += b < (int)blockIdx.x ? h : 0;
+      }
+    }
+  }
+  int inc = total;  // inclusive sum over the experts: in the wave, then across the waves
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 63) wsum[w] = inc;
+  __syncthreads();
+  for (int v = 0; v < w; ++v) inc += wsum[v];
+  if (tid < E) {
+    if (blockIdx.x == 0) {
+      if (tid == 0) offsets[0] = 0;
+      offsets[tid + 1] = inc;
+    }
+    int next = inc - total + before;
+    for (int v = 0; v < kPlanWaves; ++v) {
+      const int c = cnt[v * stride + tid];
+      cnt[v * stride + tid] = next;
+      next += c;
+    }
+  }
+  __syncthreads();
+  for (int r = 0; r < rounds; ++r) {
+    const int64_t i = i0 + 64 * r + lane;
+    const int id = plan_id(ids, i, iend, E);
+    const uint64_t m = same_id(id, bits), below = m & ((1ull << lane) - 1);
+    const int at = my[id] + __popcll(below);
+    wave_sync();
+    if (below == 0) my[id] = at + __popcll(m);
+    wave_sync();
+    if (i < iend) {
+      pos[i] = id < E ? at : -1;
+      if (id < E) order[at] = (int32_t)i;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// First low-rank stage of sorted rows: T[p] = X[token(p)] L1_e for the tile's
+// 16 RT rows, QS 16-column slices and the k-chunk of the block, on
+// v_mfma_f32_16x16x32_bf16 (lane l: row or column l % 16, the 8 k at
+// 8 (l / 16)).  The four waves take the 32-k steps round-robin, U of them in
+// flight; their partials are summed through LDS in wave order.
+// Few rows per expert (RT = 1): L1_e is what is read (r_pad d values per
+// tile), so k is split over blocks and the partials are summed by the product
+// kernel.  Many rows (RT = 4): 64 rows share each read of L1_e.
+// ---------------------------------------------------------------------------
+template <typename XT, int RT, int QS, bool EX>
+__global__ __launch_bounds__(256) void k_expert_t(const XT* __restrict__ X, int d, const uint8_t* __restrict__ lowrank,
+                                                  int64_t lr_stride, int r_pad, Segments s, ExpertTPlan pl,
+                                                  float* __restrict__ Tp, bf16_t* __restrict__ T, int tparts) {
+  constexpr int U = RT == 4 ? 2 : 4, COLS = 16 * QS;
+  __shared__ float sP[4][16 * RT][COLS + 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+  int b = blockIdx.x;
+  const int cg = b % pl.ncg;
+  b /= pl.ncg;
+  const int c = b % pl.nchunk, t = b / pl.nchunk;
+  RowTile rt;
+  if (EX) {
+    rt = expert_tile<16 * RT>(s, t);
+    if (rt.rows == 0) return;
+  } else {
+    rt = RowTile{0, 16 * RT * t, min(16 * RT, s.P - 16 * RT * t)};
+  }
+  const XT* xr[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    xr[i] = X + (size_t)row_token(s, rt.row0 + min(16 * i + lr, rt.rows - 1)) * d + 8 * lg;
+  const bf16_t* lp = reinterpret_cast<const bf16_t*>(lowrank + rt.e * lr_stride) + (size_t)(COLS * cg + lr) * d + 8 * lg;
+  const int s0 = c * pl.ksteps, s1 = min(d >> 5, s0 + pl.ksteps);
+
+  f32x4 acc[RT][QS];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int q = 0; q < QS; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int sb = s0 + w; sb < s1; sb += 4 * U) {
+    uint4 xa[U][RT], lb[U][QS];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = 32 * min(sb + 4 * u, s1 - 1);  // clamped: masked below
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float v[8];
+        Load8<XT>::load(xr[i] + k, v, xa[u][i]);
+      }
+#pragma unroll
+      for (int q = 0; q < QS; ++q) lb[u][q] = *reinterpret_cast<const uint4*>(lp + (size_t)16 * q * d + k);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (sb + 4 * u < s1) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < QS; ++q)
+            acc[i][q] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xa[u][i]), as_bf16x8(lb[u][q]), acc[i][q], 0, 0, 0);
+      }
+  }
+  // 16x16 result layout: lane l, element i -> row 4 (l / 16) + i, column l % 16
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int q = 0; q < QS; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sP[w][16 * i + 4 * lg + e][16 * q + lr] = acc[i][q][e];
+  __syncthreads();
+  for (int e = tid; e < rt.rows * COLS; e += 256) {
+    const int rr = e / COLS, cc = e % COLS;
+    float v = sP[0][rr][cc] + sP[1][rr][cc] + sP[2][rr][cc] + sP[3][rr][cc];
+    const size_t p = (size_t)rt.row0 + rr;
+    if (Tp) {
+      Tp[((size_t)c * s.P + p) * r_pad + COLS * cg + cc] = v;
+    } else {
+      for (int part = 0; part < tparts; ++part) {
+        const uint32_t h = f32_to_bf16_bits(v);
+        T[(p * tparts + part) * r_pad + COLS * cg + cc] = (bf16_t)h;
+        v -= bf16_to_f32((bf16_t)h);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combination: Y[t] = residual[t] + sum_j w[t][j] Z[pos[t][j]], fp32 in order
+// of j and one rounding.  Dropped pairs (pos outside 0 .. P - 1) add nothing,
+// whatever their weight or the rows of Z hold.  Bound by reading Z: VEC
+// columns (16 bytes of bf16) per thread and up to 8 rows in flight; the
+// token's positions and weights are the same for the whole block.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    uint4 raw;
+    Load8<T>::load(p, v, raw);
+  } else if constexpr (sizeof(T) == 2) {
+    v[0] = bf16_to_f32(*p);
+  } else {
+    v[0] = *p;
+  }
+}
+
+template <typename ZT, typename WT, int VEC>
+__global__ __launch_bounds__(256) void k_combine(const ZT* __restrict__ Z, int topk, int m, int P,
+                                                 const int32_t* __restrict__ pos, const WT* __restrict__ wt,
+                                                 const void* res, int res_bf16, void* Y, int y_bf16) {
+  const int t = blockIdx.x;
+  const int c = (blockIdx.y * 256 + threadIdx.x) * VEC;
+  if (c >= m) return;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  const size_t o = (size_t)t * m + c;
+  if (res) {
+    if (res_bf16)
+      load_vec<bf16_t, VEC>((const bf16_t*)res + o, acc);
+    else
+      load_vec<float, VEC>((const float*)res + o, acc);
+  }
+  constexpr int J = 8;
+  for (int j0 = 0; j0 < topk; j0 += J) {
+    float z[J][VEC], w[J];
+    bool on[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int jj = min(j0 + j, topk - 1);
+      const int p = pos[(size_t)t * topk + jj];
+      on[j] = j0 + j < topk && p >= 0 && p < P;
+      float wv[1];
+      load_vec<WT, 1>(wt + (size_t)t * topk + jj, wv);
+      w[j] = wv[0];
+      if (on[j]) load_vec<ZT, VEC>(Z + (size_t)p * m + c, z[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (on[j]) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(w[j], z[j][i], acc[i]);
+      }
+  }
+  if (y_bf16) {
+    bf16_t* y = (bf16_t*)Y + o;
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint4*>(y) = uint4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                           pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])};
+    else
+      *y = (bf16_t)(pack_bf16x2(acc[0], acc[0]) & 0xFFFFu);
+  } else {
+    float* y = (float*)Y + o;
+    if constexpr (VEC == 8) {
+      reinterpret_cast<float4*>(y)[0] = float4{acc[0], acc[1], acc[2], acc[3]};
+      reinterpret_cast<float4*>(y)[1] = float4{acc[4], acc[5], acc[6], acc[7]};
+    } else {
+      *y = acc[0];
+    }
+  }
+}
+
+template <typename I>
+hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* pos, void* ws,
+                  hipStream_t st) {
+  int bits = 1;
+  while ((1 << bits) <= E) ++bits;  // ids 0 .. E
+  const unsigned lds = (unsigned)(kPlanWaves * (E + 1) * 4);
+  if (P <= kPlanOne) {
+    launch_kernel(k_plan<I, true>, dim3(1), dim3(kPlanThreads), lds, st, ids, P, E, bits, (const int32_t*)nullptr, offsets,
+                  order, pos);
+    return hipGetLastError();
+  }
+  const unsigned blocks = (unsigned)((P + kPlanChunk - 1) / kPlanChunk);
+  launch_kernel(k_plan_hist<I>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, P, E, (int32_t*)ws);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  launch_kernel(k_plan<I, false>, dim3(blocks), dim3(kPlanThreads), lds, st, ids, P, E, bits, (const int32_t*)ws, offsets,
+                order, pos);
+  return hipGetLastError();
+}
+
+template <typename XT, bool EX>
+hipError_t expert_t(const XT* X, int d, const uint8_t* lowrank, int64_t lr_stride, int r_pad, const Segments& s,
+                    const ExpertTPlan& p, float* Tp, bf16_t* T, int tparts, hipStream_t st) {
+  const int64_t blocks = (int64_t)p.tiles * p.nchunk * p.ncg;
+  if (blocks <= 0 || blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(256);
+#define TQ_ET(RT, QS) launch_kernel(k_expert_t<XT, RT, QS, EX>, grid, block, 0, st, X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts)
+  if (p.rt == 1) {
+    if (p.qs == 2) TQ_ET(1, 2); else TQ_ET(1, 4);
+  } else {
+    if (p.qs == 2) TQ_ET(4, 2); else TQ_ET(4, 4);
+  }
+#undef TQ_ET
+  return hipGetLastError();
+}
+
+template <typename ZT, typename WT>
+hipError_t combine_t(const void* Z, int n, int topk, int m, int P, const int32_t* pos, const void* w, const void* res,
+                     bool res_bf16, void* Y, bool y_bf16, hipStream_t st) {
+  if (m % 8 == 0)
+    launch_kernel(k_combine<ZT, WT, 8>, dim3((unsigned)n, (unsigned)((m + 2047) / 2048)), dim3(256), 0, st, (const ZT*)Z, topk,
+                  m, P, pos, (const WT*)w, res, res_bf16 ? 1 : 0, Y, y_bf16 ? 1 : 0);
+  else
+    launch_kernel(k_combine<ZT, WT, 1>, dim3((unsigned)n, (unsigned)((m + 255) / 256)), dim3(256), 0, st, (const ZT*)Z, topk, m,
+                  P, pos, (const WT*)w, res, res_bf16 ? 1 : 0, Y, y_bf16 ? 1 : 0);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t expert_plan_ws_bytes(int64_t P, int E) {
+  return P <= kPlanOne ? 0 : (size_t)((P + kPlanChunk - 1) / kPlanChunk) * (size_t)E * 4;
+}
+
+hipError_t launch_expert_plan(const void* ids, bool i64, int64_t P, int E, int32_t* offsets, int32_t* order,
+                              int32_t* pos, void* ws, hipStream_t st) {
+  return i64 ? plan_t((const int64_t*)ids, P, E, offsets, order, pos, ws, st)
+             : plan_t((const int32_t*)ids, P, E, offsets, order, pos, ws, st);
+}
+
+ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
+  ExpertTPlan p{};
+  const int nq = r_pad / 16, steps = d / 32;
+  p.qs = std::min(nq, 4);
+  p.ncg = nq / p.qs;
+  p.rt = partial ? 1 : 4;
+  p.tiles = (int)(E > 0 ? max_expert_tiles(P, E, 16 * p.rt) : (P + 16 * p.rt - 1) / (16 * p.rt));
+  // partial: chunks of 16 steps (512 k), at most 8 of them for the product kernel to sum
+  p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 8)) : 1;
+  p.ksteps = (steps + p.nchunk - 1) / p.nchunk;
+  p.nchunk = (steps + p.ksteps - 1) / p.ksteps;
+  return p;
+}
+
+hipError_t launch_expert_t(const void* X, bool bf16, int d, const uint8_t* lowrank, int64_t lr_stride, int r_pad,
+                           const Segments& s, bool experts, const ExpertTPlan& p, float* Tp, bf16_t* T, int tparts,
+                           hipStream_t st) {
+  if (bf16)
+    return experts ? expert_t<bf16_t, true>((const bf16_t*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st)
+                   : expert_t<bf16_t, false>((const bf16_t*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st);
+  return experts ? expert_t<float, true>((const float*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st)
+                 : expert_t<float, false>((const float*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st);
+}
+
+hipError_t launch_expert_combine(const void* Z, bool z_bf16, int n, int topk, int m, int64_t P, const int32_t* pos,
+                                 const void* w, bool w_bf16, const void* res, bool res_bf16, void* Y, bool y_bf16,
+                                 hipStream_t st) {
+  const int p = (int)P;
+  if (z_bf16)
+    return w_bf16 ? combine_t<bf16_t, bf16_t>(Z, n, topk, m, p, pos, w, res, res_bf16, Y, y_bf16, st)
+                  : combine_t<bf16_t, float>(Z, n, topk, m, p, pos, w, res, res_bf16, Y, y_bf16, st);
+  return w_bf16 ? combine_t<float, bf16_t>(Z, n, topk, m, p, pos, w, res, res_bf16, Y, y_bf16, st)
+                : combine_t<float, float>(Z, n, topk, m, p, pos, w, res, res_bf16, Y, y_bf16, st);
+}
+
+}  // namespace tq

@@ -16,10 +16,11 @@ import torch
 from .build import LIB
 
 TQ_F32, TQ_BF16 = 0, 1
+TQ_ACT_NONE, TQ_ACT_RELU, TQ_ACT_SILU, TQ_ACT_GELU, TQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 
 _STATUS = {
     0: "TQ_OK", -1: "TQ_ERR_NULL", -2: "TQ_ERR_SHAPE", -3: "TQ_ERR_DTYPE", -4: "TQ_ERR_BITS",
-    -5: "TQ_ERR_ALIGN", -6: "TQ_ERR_WORKSPACE", -7: "TQ_ERR_HIP",
+    -5: "TQ_ERR_ALIGN", -6: "TQ_ERR_WORKSPACE", -7: "TQ_ERR_HIP", -8: "TQ_ERR_ACT",
 }
 
 EXPORTS = (
@@ -35,6 +36,8 @@ EXPORTS = (
     "tq_linear_asym_debug", "tq_linear_mp_asym_debug", "tq_linear_qlr_debug", "tq_linear_noalloc",
     "tq_debug_linear_handoff",
     "tq_debug_stream_read", "tq_debug_mfma_ceiling", "tq_debug_accumulate_i8", "tq_debug_gemm_w4a4",
+    "tq_linear_act_workspace_bytes", "tq_linear_act", "tq_expert_plan_workspace_bytes", "tq_expert_plan",
+    "tq_linear_experts_workspace_bytes", "tq_linear_experts", "tq_expert_combine",
 )
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # TQ_NOALLOC_SCRATCH_BYTES of include/tq.h
@@ -121,6 +124,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                          ctypes.c_uint, c_int, ptr]),
         "tq_debug_stream_read": (st, [ptr, sz, ptr, c_int, ptr]),
         "tq_debug_mfma_ceiling": (st, [c_int, c_int, ptr, ptr]),
+        "tq_linear_act_workspace_bytes": (sz, [i64, i64, i64, i64]),
+        "tq_linear_act": (st, [ptr, c_int, i64, i64, i64, i64, ptr, ptr, ptr, ptr, c_int, c_int, ptr, c_int, ptr, c_int,
+                               ptr, sz, ptr]),
+        "tq_expert_plan_workspace_bytes": (sz, [i64, i64, i64]),
+        "tq_expert_plan": (st, [ptr, c_int, i64, i64, i64, ptr, ptr, ptr, ptr, sz, ptr]),
+        "tq_linear_experts_workspace_bytes": (sz, [i64, i64, i64, i64, i64, i64]),
+        "tq_linear_experts": (st, [ptr, c_int, i64, i64, i64, i64, i64, i64, ptr, ptr, ptr, ptr, ptr, ptr, c_int, c_int,
+                                   ptr, c_int, ptr, sz, ptr]),
+        "tq_expert_combine": (st, [ptr, c_int, i64, i64, i64, i64, ptr, ptr, c_int, ptr, c_int, ptr, c_int, ptr]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -509,6 +521,151 @@ def tq_linear_asym(X, w_codes, s_w, colsum, lowrank, m: int, r: int, y_dtype=tor
     else:
         _check("tq_linear_asym", lib.tq_linear_asym(_p(X), _dt(X), n, d, m, r, _p(w_codes), _p(s_w), _p(colsum),
                                                     _p(lowrank), _p(Y), _dt(Y), _p(ws), ws.numel(), _stream(X)))
+    return Y
+
+
+def _need_shape(name, t, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {shape}")
+
+
+def _need_dtype(name, t, *dtypes):
+    if t is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def _need_elems(name, t, count):
+    if t is not None and t.numel() * t.element_size() < count:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, expected at least {count}")
+
+
+def _need_device(ref, *ts):
+    _need_cuda(ref, *ts)
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise ValueError("tensors must be on one device")
+
+
+def linear_act_workspace(n: int, d: int, m: int, r: int, device) -> torch.Tensor:
+    """A zero-filled workspace for tq_linear_act."""
+    return torch.zeros(max(1, load().tq_linear_act_workspace_bytes(n, d, m, r)), dtype=torch.uint8, device=device)
+
+
+def _layer_args(X, E, w_codes, s_w, lowrank, m, r, bias, gated):
+    """Checks of the stacked weights of E layers of m channels on inputs of X's width."""
+    d = X.shape[1]
+    _need_shape("w_codes", w_codes, E * m, d // 2)
+    _need_shape("s_w", s_w, E * m)
+    _need_shape("bias", bias, E * m)
+    _need_dtype("s_w", s_w, torch.float32)
+    _need_dtype("bias", bias, torch.float32)
+    _need_dtype("w_codes", w_codes, torch.uint8, torch.int8)
+    if r > 0 and lowrank is not None:
+        _need_elems("lowrank", lowrank, E * load().tq_lowrank_bytes(d, m, r))
+    return m // 2 if gated else m
+
+
+def tq_linear_act(X, w_codes, s_w, lowrank, m: int, r: int, bias=None, act: int = TQ_ACT_NONE, gated: bool = False,
+                  residual=None, y_dtype=torch.bfloat16, Y=None, ws=None):
+    """Y = act(v) + residual, v = s_x s_w (Q4(X) Q4(R)) + (X L1) L2 + bias; gated: act of the first m / 2 channels
+    times the others.  ``act``: TQ_ACT_*; ``residual`` may be Y."""
+    lib = load()
+    _need_device(X, w_codes, s_w, lowrank, bias, residual, Y, ws)
+    n, d = X.shape
+    mo = _layer_args(X, 1, w_codes, s_w, lowrank, m, r, bias, gated)
+    if Y is None:
+        Y = torch.empty((n, mo), dtype=y_dtype, device=X.device)
+    _need_shape("Y", Y, n, mo)
+    _need_shape("residual", residual, n, mo)
+    if ws is None:
+        ws = linear_act_workspace(n, d, m, r, X.device)
+    with torch.cuda.device(X.device):
+        _check("tq_linear_act", lib.tq_linear_act(
+            _p(X), _dt(X), n, d, m, r, _p(w_codes), _p(s_w), _p(lowrank), _p(bias), int(act), 1 if gated else 0,
+            _p(residual), TQ_BF16 if residual is None else _dt(residual), _p(Y), _dt(Y), _p(ws), ws.numel(), _stream(X)))
+    return Y
+
+
+def expert_plan_workspace(n: int, topk: int, E: int, device) -> torch.Tensor:
+    """Scratch for tq_expert_plan (its contents on entry are ignored)."""
+    return torch.empty(max(1, load().tq_expert_plan_workspace_bytes(n, topk, E)), dtype=torch.uint8, device=device)
+
+
+def tq_expert_plan(ids, E: int, offsets=None, order=None, pos=None, ws=None):
+    """Pairs of ids (n x topk, int32 or int64) sorted by expert -> (offsets E + 1, order n topk, pos n x topk), int32.
+    Ids outside 0 .. E - 1 are dropped (pos -1)."""
+    lib = load()
+    _need_device(ids, offsets, order, pos, ws)
+    _need_dtype("ids", ids, torch.int32, torch.int64)
+    n, topk = ids.shape
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+    if order is None:
+        order = torch.empty(n * topk, dtype=torch.int32, device=ids.device)
+    if pos is None:
+        pos = torch.empty((n, topk), dtype=torch.int32, device=ids.device)
+    if ws is None:
+        ws = expert_plan_workspace(n, topk, E, ids.device)
+    _need_shape("offsets", offsets, E + 1)
+    _need_shape("order", order, n * topk)
+    _need_shape("pos", pos, n, topk)
+    for name, t in (("offsets", offsets), ("order", order), ("pos", pos)):
+        _need_dtype(name, t, torch.int32)
+    with torch.cuda.device(ids.device):
+        _check("tq_expert_plan", lib.tq_expert_plan(_p(ids), 8 * ids.element_size(), n, topk, E, _p(offsets), _p(order),
+                                                    _p(pos), _p(ws), ws.numel(), _stream(ids)))
+    return offsets, order, pos
+
+
+def linear_experts_workspace(n: int, topk: int, d: int, m: int, r: int, E: int, device) -> torch.Tensor:
+    """A zero-filled workspace for tq_linear_experts."""
+    return torch.zeros(max(1, load().tq_linear_experts_workspace_bytes(n, topk, d, m, r, E)), dtype=torch.uint8,
+                       device=device)
+
+
+def tq_linear_experts(X, w_codes, s_w, lowrank, m: int, r: int, offsets, order=None, topk: int = 1, bias=None,
+                      act: int = TQ_ACT_NONE, gated: bool = False, y_dtype=torch.bfloat16, Y=None, ws=None):
+    """tq_linear_act on rows sorted by expert (tq_expert_plan): row p takes token order[p] // topk of X, or row p of X
+    when ``order`` is None, and the weights of its expert (E stacked layers).  Rows of Y from offsets[E] on are left
+    as they were (unspecified when Y is allocated here)."""
+    lib = load()
+    _need_device(X, w_codes, s_w, lowrank, offsets, order, bias, Y, ws)
+    n, d = X.shape
+    E = offsets.shape[0] - 1
+    mo = _layer_args(X, E, w_codes, s_w, lowrank, m, r, bias, gated)
+    if order is None and topk != 1:
+        raise ValueError("topk without order")
+    _need_shape("order", order, n * topk)
+    for name, t in (("offsets", offsets), ("order", order)):
+        _need_dtype(name, t, torch.int32)
+    if Y is None:
+        Y = torch.empty((n * topk, mo), dtype=y_dtype, device=X.device)
+    _need_shape("Y", Y, n * topk, mo)
+    if ws is None:
+        ws = linear_experts_workspace(n, topk, d, m, r, E, X.device)
+    with torch.cuda.device(X.device):
+        _check("tq_linear_experts", lib.tq_linear_experts(
+            _p(X), _dt(X), n, topk, d, m, r, E, _p(offsets), _p(order), _p(w_codes), _p(s_w), _p(lowrank), _p(bias),
+            int(act), 1 if gated else 0, _p(Y), _dt(Y), _p(ws), ws.numel(), _stream(X)))
+    return Y
+
+
+def tq_expert_combine(Z, pos, weights, residual=None, y_dtype=torch.bfloat16, Y=None):
+    """Y[t] = residual[t] + sum_j weights[t, j] Z[pos[t, j]] (pairs with pos outside Z's rows add nothing)."""
+    lib = load()
+    _need_device(Z, pos, weights, residual, Y)
+    rows, m = Z.shape
+    n, topk = pos.shape
+    _need_dtype("pos", pos, torch.int32)
+    _need_shape("weights", weights, n, topk)
+    if Y is None:
+        Y = torch.empty((n, m), dtype=y_dtype, device=Z.device)
+    _need_shape("Y", Y, n, m)
+    _need_shape("residual", residual, n, m)
+    with torch.cuda.device(Z.device):
+        _check("tq_expert_combine", lib.tq_expert_combine(
+            _p(Z), _dt(Z), rows, n, topk, m, _p(pos), _p(weights), _dt(weights), _p(residual),
+            TQ_BF16 if residual is None else _dt(residual), _p(Y), _dt(Y), _stream(Z)))
     return Y
 
 
