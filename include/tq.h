@@ -526,8 +526,8 @@ tq_status tq_expert_plan(const void* ids, int ids_bits, int64_t n, int64_t topk,
  *   ws       tq_linear_experts_workspace_bytes(n, topk, d, m, r, E) bytes,
  *            zero-filled once before its first use; calls that share it must
  *            be ordered.
- * Shapes as tq_linear_act and tq_expert_plan, with n topk <= 2^24 and
- * n d < 2^31.  Errors as tq_linear_act.
+ * Shapes as tq_linear_act and tq_expert_plan, with E m <= 2^30 and, with
+ * order, n d < 2^31.  Errors as tq_linear_act.
  */
 size_t tq_linear_experts_workspace_bytes(int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E);
 tq_status tq_linear_experts(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r,

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
 SOURCES = ["tq_api.hip", "tq_quant.hip", "tq_gemm.hip", "tq_gemm8.hip", "tq_decode.hip", "tq_rht.hip", "tq_qlr.hip", "tq_asym.hip",
-           "tq_act.hip", "tq_expert.hip"]
+           "tq_act.hip", "tq_act_tile.hip", "tq_expert.hip"]
 ARCH = "gfx950"
 
 

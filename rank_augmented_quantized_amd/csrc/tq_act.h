@@ -54,6 +54,7 @@ struct ActArgs {
   void* Y;
   int y_bf16;
   Segments seg;
+  const int4* map;  // tile kernel, experts: table of row tiles
 };
 
 // The tile of up to TM consecutive rows of one expert that has index t among
@@ -94,7 +95,7 @@ __device__ __forceinline__ RowTile expert_tile(const Segments& s, int t) {
   return RowTile{0, 0, 0};
 }
 // Most such tiles: every expert with rows has at most one that is not full.
-inline int64_t max_expert_tiles(int64_t P, int64_t E, int64_t TM) { return P / TM + (E < P ? E : P); }
+__host__ __device__ inline int64_t max_expert_tiles(int64_t P, int64_t E, int64_t TM) { return P / TM + (E < P ? E : P); }
 
 // Token of sorted row p (p inside 0 .. P - 1).
 __device__ __forceinline__ int row_token(const Segments& s, int p) {
@@ -125,33 +126,63 @@ __device__ __forceinline__ float gelu_erf(float x) {
 // very negative arguments and the quotient is then -0, as the limit.
 __device__ __forceinline__ float x_sigmoid(float x, float u) { return x * __builtin_amdgcn_rcpf(1.0f + __expf(-u)); }
 
-__device__ __forceinline__ float activate(float v, int act) {
+// The activation of four values (one branch for the four).
+__device__ __forceinline__ void activate4(float (&v)[4], int act) {
   switch (act) {
-    case ACT_RELU: return v < 0.0f ? 0.0f : v;
-    case ACT_SILU: return x_sigmoid(v, v);
-    case ACT_GELU: return gelu_erf(v);
-    case ACT_GELU_TANH: return x_sigmoid(v, 1.5957691216057308f * __builtin_fmaf(0.044715f * v * v, v, v));
-    default: return v;
+    case ACT_RELU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = v[q] < 0.0f ? 0.0f : v[q];
+      break;
+    case ACT_SILU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = x_sigmoid(v[q], v[q]);
+      break;
+    case ACT_GELU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = gelu_erf(v[q]);
+      break;
+    case ACT_GELU_TANH:
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = x_sigmoid(v[q], 1.5957691216057308f * __builtin_fmaf(0.044715f * v[q] * v[q], v[q], v[q]));
+      break;
+    default: break;
   }
 }
 
-// k-chunk split of the first low-rank stage in the rows kernel's case.
+// Work split of the experts' first low-rank stage.
 struct ExpertTPlan {
-  int rt;      // 16-row groups per block (1 or 4)
+  int rt;      // 16-row groups per block: 1 (rows product, k-chunk partials) or 4 (tile product)
   int qs;      // 16-column slices per block
   int ncg;     // column groups of 16 qs
   int ksteps;  // 32-k steps per chunk
   int nchunk;
   int tiles;   // row tiles (upper bound)
 };
-
-hipError_t launch_rows_act(const ActArgs& a, bool gated, bool experts, hipStream_t st);
-// First low-rank stage of sorted rows, T[p] = X[token(p)] L1_e: fp32 partials
-// per k-chunk (Tp) when the plan is partial, else tparts bf16 parts to T.
 ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial);
-hipError_t launch_expert_t(const void* X, bool bf16, int d, const uint8_t* lowrank, int64_t lr_stride, int r_pad,
-                           const Segments& s, bool experts, const ExpertTPlan& p, float* Tp, bf16_t* T, int tparts,
-                           hipStream_t st);
+struct ExpertPrologue {
+  const void* X;
+  int d;
+  uint8_t* xc;  // per token: codes and scale
+  float* sx;
+  const uint8_t* lowrank;
+  int64_t lr_stride;
+  int r_pad, tparts;
+  Segments seg;
+  ExpertTPlan t;
+  float* Tp;  // rows product: partials of T
+  bf16_t* T;  // tile product: T in bf16 parts
+  int4* map;  // tile product: table of row tiles of map_rows rows
+  int map_rows;
+  int nqb;    // set by the launcher
+};
+hipError_t launch_expert_prologue(const ExpertPrologue& p, bool bf16, bool packed, hipStream_t st);
+// The product and its epilogue: up to 16 rows per tile, bound by the weights
+// (codes nibble-packed), or 256 channels by up to 256 rows (int8-order codes).
+hipError_t launch_rows_act(const ActArgs& a, bool gated, bool experts, hipStream_t st);
+hipError_t launch_tile_act(const ActArgs& a, bool gated, bool experts, hipStream_t st);
+// Rows per tile of launch_tile_act for M rows of E experts (E = 0: one layer) and N weight channels.
+int tile_act_rows(int64_t M, int64_t E);
 // Routing plan and combination (tq_expert.hip).
 size_t expert_plan_ws_bytes(int64_t P, int E);
 hipError_t launch_expert_plan(const void* ids, bool i64, int64_t P, int E, int32_t* offsets, int32_t* order,

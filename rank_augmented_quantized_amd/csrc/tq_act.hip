@@ -153,13 +153,14 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 4 : 2) void k_rows_act(Act
       v[h][i] = (float)(s >> 8) * (sx[i] * sw) + lr[i] + bias;
     }
   }
+  activate4(v[0], g.act);
   if (oc >= NO) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = 4 * lg + i;
     if (row >= rt.rows) break;
     const size_t o = (size_t)(rt.row0 + row) * NO + oc;
-    float y = activate(v[0][i], g.act);
+    float y = v[0][i];
     if (GATED) y *= v[GATED ? 1 : 0][i];
     if (g.res) y += g.res_bf16 ? bf16_to_f32(((const bf16_t*)g.res)[o]) : ((const float*)g.res)[o];
     if (g.y_bf16)

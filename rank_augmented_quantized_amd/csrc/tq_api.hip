@@ -1172,28 +1172,48 @@ constexpr int64_t kMaxTopk = 64;
 
 // Workspace of tq_linear_act (E = 0) and tq_linear_experts: the hand-off and
 // counter regions at the fixed offsets of tq_linear's, then per token its
-// scale and codes, per row the partials of T.
+// scale and codes, per row T or its partials, and the table of row tiles.
 struct ActWs {
-  size_t sx, xc, p, total;
-  int r_pad;
-  tq::ExpertTPlan tplan;
+  size_t sx, xc, t, p, map, total;
+  int r_pad, tile_rows;
+  bool small;  // the rows product (nibble-packed codes), else the tile product
+  tq::ProloguePlan plan;    // one layer
+  tq::ExpertTPlan tplan;    // experts
 };
+// Experts with at most this many rows on average take the rows product.
+constexpr int64_t kSmallExpertRows = 8;
+
 ActWs act_ws(int64_t n, int64_t topk, int64_t d, int64_t r, int64_t E) {
   ActWs w{};
   const int64_t P = n * topk;
   w.r_pad = (int)r_padded(r);
-  size_t psize = 0;
-  if (w.r_pad > 0 && P > 0) {
-    w.tplan = tq::plan_expert_t(P, (int)E, (int)d, w.r_pad, true);
-    psize = (size_t)w.tplan.nchunk * (size_t)P * (size_t)w.r_pad * 4;
+  w.small = P <= std::max<int64_t>(kSmallN, kSmallExpertRows * E);
+  size_t psize = 0, msize = 0;
+  if (E == 0) {
+    w.plan = tq::plan_prologue((int)n, (int)d, w.r_pad, w.small,
+                               w.small ? tq::gemv_max_chunks((int)n, (int)(d / 2), w.r_pad) : 1);
+    if (w.plan.ntb > 0 && (w.plan.nchunk > 1 || w.plan.partial))
+      psize = (size_t)w.plan.nchunk * (size_t)n * (size_t)w.r_pad * 4;
+  } else {
+    w.tplan = tq::plan_expert_t(P, (int)E, (int)d, w.r_pad, w.small);
+    if (w.small) {
+      psize = (size_t)w.tplan.nchunk * (size_t)P * (size_t)w.r_pad * 4;
+    } else {
+      w.tile_rows = tq::tile_act_rows(P, E);
+      msize = 16 * (size_t)(1 + tq::max_expert_tiles(P, E, w.tile_rows));
+    }
   }
   size_t o = tq::kSyncBytes + kCtrBytes;
   w.sx = o;
   o = align256(o + (size_t)n * 4);
   w.xc = o;
-  o = align256(o + (size_t)n * (size_t)(d / 2));
+  o = align256(o + (size_t)n * (size_t)(w.small ? d / 2 : d));
+  w.t = o;  // the largest number of parts, whatever Y's type
+  o = align256(o + (w.small && E > 0 ? 0 : (size_t)P * (size_t)w.r_pad * 2 * tq::kMaxTParts));
   w.p = o;
   o = align256(o + psize);
+  w.map = o;
+  o = align256(o + msize);
   w.total = o;
   return w;
 }
@@ -1203,7 +1223,7 @@ bool act_shape_ok(int64_t n, int64_t d, int64_t m, int64_t r) {
 }
 bool experts_shape_ok(int64_t n, int64_t topk, int64_t d, int64_t m, int64_t r, int64_t E) {
   return act_shape_ok(n, d, m, r) && topk >= 1 && topk <= kMaxTopk && E >= 1 && E <= tq::kMaxExperts &&
-         n <= kMaxPairs / topk && n * d < ((int64_t)1 << 31) && E * m <= kMaxDim;
+         n <= kMaxPairs / topk && E * m <= kMaxDim;
 }
 bool valid_act(tq_act a) { return a >= TQ_ACT_NONE && a <= TQ_ACT_GELU_TANH; }
 
@@ -1213,14 +1233,22 @@ tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t
                   tq_dtype res_dt, void* Y, tq_dtype y_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
   const ActWs L = act_ws(n, topk, d, r, E);
   if (ws_bytes < L.total) return TQ_ERR_WORKSPACE;
+  // the fixed counter region holds every counter this shape uses
+  if ((size_t)L.plan.counters * 4 > kCtrBytes) return TQ_ERR_SHAPE;
   uint8_t* base = (uint8_t*)ws;
   const bool xb = x_dt == TQ_BF16, ex = E > 0;
+  uint8_t* xc = base + L.xc;
+  float* sx = (float*)(base + L.sx);
+  float* P = (float*)(base + L.p);
+  tq::bf16_t* T = (tq::bf16_t*)(base + L.t);
+  int4* map = (int4*)(base + L.map);
   tq::ActArgs a{};
-  a.A = base + L.xc;
-  a.sx = (const float*)(base + L.sx);
+  a.A = xc;
+  a.sx = sx;
   a.B = (const uint8_t*)w_codes;
   a.sw = s_w;
-  a.lda = a.ldb = d / 2;
+  a.lda = L.small ? d / 2 : d;
+  a.ldb = d / 2;
   a.M = (int)(n * topk);
   a.N = (int)m;
   a.Kb = (int)(d / 2);
@@ -1229,8 +1257,9 @@ tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t
   a.l2_off = (int64_t)L.r_pad * d * 2;
   a.r_pad = L.r_pad;
   a.tparts = y_dt == TQ_F32 ? 3 : 2;
-  a.Tp = (const float*)(base + L.p);
-  a.nchunk = L.tplan.nchunk;
+  a.Tp = P;
+  a.nchunk = ex ? L.tplan.nchunk : (L.plan.partial ? L.plan.nchunk : 1);
+  a.T = T;
   a.bias = bias;
   a.res = residual;
   a.res_bf16 = res_dt == TQ_BF16;
@@ -1238,14 +1267,33 @@ tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t
   a.Y = Y;
   a.y_bf16 = y_dt == TQ_BF16;
   a.seg = tq::Segments{offsets, order, (int)E, (int)(n * topk), (int)topk, (int)n};
-  TQ_RUN("quant_rows", stream,
-         tq::launch_quant_rows_fast(X, xb, (int)n, (int)d, (int)d, 4, 4, base + L.xc, (float*)(base + L.sx), nullptr,
-                                    nullptr, stream));
-  if (L.r_pad)
-    TQ_RUN("lowrank_t", stream,
-           tq::launch_expert_t(X, xb, (int)d, a.lowrank, a.lr_stride, L.r_pad, a.seg, ex, L.tplan,
-                               (float*)(base + L.p), nullptr, a.tparts, stream));
-  TQ_RUN(ex ? "experts_rows" : "act_rows", stream, tq::launch_rows_act(a, gated != 0, ex, stream));
+  a.map = map;
+  if (ex) {
+    tq::ExpertPrologue p{};
+    p.X = X;
+    p.d = (int)d;
+    p.xc = xc;
+    p.sx = sx;
+    p.lowrank = a.lowrank;
+    p.lr_stride = a.lr_stride;
+    p.r_pad = L.r_pad;
+    p.tparts = a.tparts;
+    p.seg = a.seg;
+    p.t = L.tplan;
+    p.Tp = P;
+    p.T = T;
+    p.map = L.small ? nullptr : map;
+    p.map_rows = L.tile_rows;
+    TQ_RUN("experts_prologue", stream, tq::launch_expert_prologue(p, xb, L.small, stream));
+  } else {
+    TQ_RUN("prologue", stream,
+           tq::launch_prologue(X, xb, (int)n, (int)d, lowrank, L.r_pad, L.plan, xc, sx, P, T, (unsigned*)(base + tq::kSyncBytes),
+                               stream, a.tparts));
+  }
+  if (L.small)
+    TQ_RUN(ex ? "experts_rows" : "act_rows", stream, tq::launch_rows_act(a, gated != 0, ex, stream));
+  else
+    TQ_RUN(ex ? "experts_tile" : "act_tile", stream, tq::launch_tile_act(a, gated != 0, ex, stream));
   return TQ_OK;
 }
 
@@ -1304,6 +1352,8 @@ tq_status tq_linear_experts(const void* X, tq_dtype x_dt, int64_t n, int64_t top
   const tq_status st = linear_check(X, x_dt, n, d, m, r, w_codes, s_w, lowrank, Y, y_dt, ws);
   if (st != TQ_OK) return st;
   if (!experts_shape_ok(n, topk, d, m, r, E)) return TQ_ERR_SHAPE;
+  // gathered token rows are addressed by 32-bit offsets from X's codes
+  if (order && n * d >= ((int64_t)1 << 31)) return TQ_ERR_SHAPE;
   if (n == 0) return TQ_OK;
   if (!offsets) return TQ_ERR_NULL;
   if (!aligned16(offsets) || !aligned16(order) || !aligned16(bias)) return TQ_ERR_ALIGN;

@@ -34,6 +34,21 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// One value of T = X L1 (row, column col of r_pad): rounded to bf16, or, for
+// parts > 1, split into that many bf16 values, each the rounded rest, in rows
+// of parts r_pad.
+__device__ __forceinline__ void store_t(bf16_t* T, size_t row, int r_pad, int parts, int col, float v) {
+  if (parts <= 1) {
+    T[row * r_pad + col] = (bf16_t)f32_to_bf16_bits(v);
+    return;
+  }
+  for (int p = 0; p < parts; ++p) {
+    const uint32_t h = f32_to_bf16_bits(v);
+    T[(row * parts + p) * r_pad + col] = (bf16_t)h;
+    v -= bf16_to_f32((bf16_t)h);
+  }
+}
+
 // 8 consecutive activations loaded from memory as fp32 values.
 template <typename T>
 struct Load8;

@@ -136,40 +136,102 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, 
   }
 }
 
-// ---------------------------------------------------------------------------
-// First low-rank stage of sorted rows: T[p] = X[token(p)] L1_e for the tile's
-// 16 RT rows, QS 16-column slices and the k-chunk of the block, on
-// v_mfma_f32_16x16x32_bf16 (lane l: row or column l % 16, the 8 k at
-// 8 (l / 16)).  The four waves take the 32-k steps round-robin, U of them in
-// flight; their partials are summed through LDS in wave order.
-// Few rows per expert (RT = 1): L1_e is what is read (r_pad d values per
-// tile), so k is split over blocks and the partials are summed by the product
-// kernel.  Many rows (RT = 4): 64 rows share each read of L1_e.
-// ---------------------------------------------------------------------------
-template <typename XT, int RT, int QS, bool EX>
-__global__ __launch_bounds__(256) void k_expert_t(const XT* __restrict__ X, int d, const uint8_t* __restrict__ lowrank,
-                                                  int64_t lr_stride, int r_pad, Segments s, ExpertTPlan pl,
-                                                  float* __restrict__ Tp, bf16_t* __restrict__ T, int tparts) {
-  constexpr int U = RT == 4 ? 2 : 4, COLS = 16 * QS;
-  __shared__ float sP[4][16 * RT][COLS + 1];
+// The table of row tiles of TM rows: map[0].x = their number, map[1 + t] =
+// {expert, first row, rows, 0}.  One block of 256 threads; lds: kMaxExperts + 1
+// words and 4 more.
+__device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* map, int* lds) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int lr = lane & 15, lg = lane >> 4;
+  int* wsum = lds + kMaxExperts + 1;
+  int base = 0;
+  if (tid == 0) lds[0] = 0;
+  for (int e0 = 0; e0 < s.E; e0 += 256) {  // lds[e] = tiles of the experts below e
+    const int e = e0 + tid;
+    int n = 0;
+    if (e < s.E) {
+      const int a = min(max(s.offsets[e], 0), s.P), b = min(max(s.offsets[e + 1], a), s.P);
+      n = (b - a + TM - 1) / TM;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(n, d);
+      if (lane >= d) n += y;
+    }
+    if (lane == 63) wsum[w] = n;
+    __syncthreads();
+    for (int v = 0; v < w; ++v) n += wsum[v];
+    if (e < s.E) lds[e + 1] = base + n;
+    base += wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    __syncthreads();
+  }
+  const int total = min(base, (int)max_expert_tiles(s.P, s.E, TM));  // the table's size, whatever the offsets
+  if (tid == 0) map[0] = int4{total, 0, 0, 0};
+  for (int t = tid; t < total; t += 256) {
+    int lo = 0, hi = s.E - 1;  // the last expert with lds[e] <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (lds[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int a = min(max(s.offsets[lo], 0), s.P), b = min(max(s.offsets[lo + 1], a), s.P);
+    const int row0 = a + (t - lds[lo]) * TM;
+    map[1 + t] = int4{lo, row0, min(TM, b - row0), 0};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Prologue of the experts' layers, one launch of three kinds of blocks:
+//  * block 0 (tile product only): the table of row tiles -- how many there
+//    are, then expert, first row and row count of each -- so that the
+//    product's blocks find their rows with one load;
+//  * blocks [nmap, nmap + nqb): codes and s_x of four tokens, one per wave
+//    (int8 order for the tile product, PK: nibble-packed for the rows product);
+//    a token is quantised once, whatever the number of its experts;
+//  * the rest: T[p] = X[token(p)] L1_e for 16 RT rows of one expert, QS
+//    16-column slices and one k-chunk, on v_mfma_f32_16x16x32_bf16 (lane l:
+//    row or column l % 16, the 8 k at 8 (l / 16)).  The four waves take the
+//    32-k steps round-robin, U of them in flight; their partials are summed
+//    through LDS in wave order, 32 columns at a time.
+// Few rows per expert (PK, RT = 1): L1_e is what is read (r_pad d values per
+// tile), so k is split over blocks and the partials are summed by the product
+// kernel.  Many rows (RT = 4): 64 rows share each read of L1_e and T leaves
+// as bf16 parts.
+// ---------------------------------------------------------------------------
+template <typename XT, int CH, int RT, int QS, bool PK>
+__global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
+  constexpr int U = RT == 4 ? 2 : 4, COLS = 16 * QS;
+  __shared__ __attribute__((aligned(16))) float sP[4][16 * RT][33];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const Segments& s = a.seg;
+  const ExpertTPlan& pl = a.t;
+  const int d = a.d;
   int b = blockIdx.x;
+  if (a.map) {
+    if (b == 0) {
+      write_tile_map(s, a.map_rows, a.map, reinterpret_cast<int*>(sP));
+      return;
+    }
+    --b;
+  }
+  if (b < a.nqb) {
+    const int row = 4 * b + w;
+    if (row >= s.ntok) return;
+    const float sx = quant_row_i8_wave<XT, CH, PK>((const XT*)a.X + (size_t)row * d, d >> 3, lane,
+                                                   a.xc + (size_t)row * (PK ? d >> 1 : d), nullptr);
+    if (lane == 0) a.sx[row] = sx;
+    return;
+  }
+  b -= a.nqb;
+  const int lr = lane & 15, lg = lane >> 4;
   const int cg = b % pl.ncg;
   b /= pl.ncg;
   const int c = b % pl.nchunk, t = b / pl.nchunk;
-  RowTile rt;
-  if (EX) {
-    rt = expert_tile<16 * RT>(s, t);
-    if (rt.rows == 0) return;
-  } else {
-    rt = RowTile{0, 16 * RT * t, min(16 * RT, s.P - 16 * RT * t)};
-  }
+  const RowTile rt = expert_tile<16 * RT>(s, t);
+  if (rt.rows == 0) return;
   const XT* xr[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
-    xr[i] = X + (size_t)row_token(s, rt.row0 + min(16 * i + lr, rt.rows - 1)) * d + 8 * lg;
-  const bf16_t* lp = reinterpret_cast<const bf16_t*>(lowrank + rt.e * lr_stride) + (size_t)(COLS * cg + lr) * d + 8 * lg;
+    xr[i] = (const XT*)a.X + (size_t)row_token(s, rt.row0 + min(16 * i + lr, rt.rows - 1)) * d + 8 * lg;
+  const bf16_t* lp =
+      reinterpret_cast<const bf16_t*>(a.lowrank + rt.e * a.lr_stride) + (size_t)(COLS * cg + lr) * d + 8 * lg;
   const int s0 = c * pl.ksteps, s1 = min(d >> 5, s0 + pl.ksteps);
 
   f32x4 acc[RT][QS];
@@ -201,26 +263,26 @@ __global__ __launch_bounds__(256) void k_expert_t(const XT* __restrict__ X, int 
                 __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xa[u][i]), as_bf16x8(lb[u][q]), acc[i][q], 0, 0, 0);
       }
   }
-  // 16x16 result layout: lane l, element i -> row 4 (l / 16) + i, column l % 16
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int q0 = 0; q0 < QS; q0 += 2) {
+    if (q0 > 0) __syncthreads();
+    // 16x16 result layout: lane l, element i -> row 4 (l / 16) + i, column l % 16
 #pragma unroll
-    for (int q = 0; q < QS; ++q)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sP[w][16 * i + 4 * lg + e][16 * q + lr] = acc[i][q][e];
-  __syncthreads();
-  for (int e = tid; e < rt.rows * COLS; e += 256) {
-    const int rr = e / COLS, cc = e % COLS;
-    float v = sP[0][rr][cc] + sP[1][rr][cc] + sP[2][rr][cc] + sP[3][rr][cc];
-    const size_t p = (size_t)rt.row0 + rr;
-    if (Tp) {
-      Tp[((size_t)c * s.P + p) * r_pad + COLS * cg + cc] = v;
-    } else {
-      for (int part = 0; part < tparts; ++part) {
-        const uint32_t h = f32_to_bf16_bits(v);
-        T[(p * tparts + part) * r_pad + COLS * cg + cc] = (bf16_t)h;
-        v -= bf16_to_f32((bf16_t)h);
-      }
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sP[w][16 * i + 4 * lg + e][16 * q + lr] = acc[i][q0 + q][e];
+    __syncthreads();
+    for (int e = tid; e < rt.rows * 32; e += 256) {
+      const int rr = e >> 5, cc = e & 31;
+      const float v = sP[0][rr][cc] + sP[1][rr][cc] + sP[2][rr][cc] + sP[3][rr][cc];
+      const size_t p = (size_t)rt.row0 + rr;
+      const int col = COLS * cg + 16 * q0 + cc;
+      if (PK)
+        a.Tp[((size_t)c * s.P + p) * a.r_pad + col] = v;
+      else
+        store_t(a.T, p, a.r_pad, a.tparts, col, v);
     }
   }
 }
@@ -300,6 +362,7 @@ __global__ __launch_bounds__(256) void k_combine(const ZT* __restrict__ Z, int t
   }
 }
 
+
 template <typename I>
 hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* pos, void* ws,
                   hipStream_t st) {
@@ -319,20 +382,26 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
   return hipGetLastError();
 }
 
-template <typename XT, bool EX>
-hipError_t expert_t(const XT* X, int d, const uint8_t* lowrank, int64_t lr_stride, int r_pad, const Segments& s,
-                    const ExpertTPlan& p, float* Tp, bf16_t* T, int tparts, hipStream_t st) {
-  const int64_t blocks = (int64_t)p.tiles * p.nchunk * p.ncg;
-  if (blocks <= 0 || blocks > INT32_MAX) return hipErrorInvalidValue;
+template <typename XT, int CH, bool PK>
+hipError_t prologue_t(const ExpertPrologue& a, hipStream_t st) {
+  const int64_t blocks = (a.map ? 1 : 0) + (int64_t)a.nqb + (a.r_pad ? (int64_t)a.t.tiles * a.t.nchunk * a.t.ncg : 0);
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (blocks == 0) return hipSuccess;
+  constexpr int RT = PK ? 1 : 4;
   const dim3 grid((unsigned)blocks), block(256);
-#define TQ_ET(RT, QS) launch_kernel(k_expert_t<XT, RT, QS, EX>, grid, block, 0, st, X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts)
-  if (p.rt == 1) {
-    if (p.qs == 2) TQ_ET(1, 2); else TQ_ET(1, 4);
-  } else {
-    if (p.qs == 2) TQ_ET(4, 2); else TQ_ET(4, 4);
-  }
-#undef TQ_ET
+  if (a.t.qs == 4)
+    launch_kernel(k_expert_prologue<XT, CH, RT, 4, PK>, grid, block, 0, st, a);
+  else
+    launch_kernel(k_expert_prologue<XT, CH, RT, 2, PK>, grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+// rows of up to 2048, 4096 or 16384 values in a wave's registers
+template <typename XT, bool PK>
+hipError_t prologue_d(const ExpertPrologue& a, hipStream_t st) {
+  if (a.d <= 2048) return prologue_t<XT, 4, PK>(a, st);
+  if (a.d <= 4096) return prologue_t<XT, 8, PK>(a, st);
+  return prologue_t<XT, 32, PK>(a, st);
 }
 
 template <typename ZT, typename WT>
@@ -361,11 +430,12 @@ hipError_t launch_expert_plan(const void* ids, bool i64, int64_t P, int E, int32
 
 ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   ExpertTPlan p{};
+  if (r_pad == 0) return p;
   const int nq = r_pad / 16, steps = d / 32;
   p.qs = std::min(nq, 4);
   p.ncg = nq / p.qs;
   p.rt = partial ? 1 : 4;
-  p.tiles = (int)(E > 0 ? max_expert_tiles(P, E, 16 * p.rt) : (P + 16 * p.rt - 1) / (16 * p.rt));
+  p.tiles = (int)max_expert_tiles(P, E, 16 * p.rt);
   // partial: chunks of 16 steps (512 k), at most 8 of them for the product kernel to sum
   p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 8)) : 1;
   p.ksteps = (steps + p.nchunk - 1) / p.nchunk;
@@ -373,14 +443,17 @@ ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   return p;
 }
 
-hipError_t launch_expert_t(const void* X, bool bf16, int d, const uint8_t* lowrank, int64_t lr_stride, int r_pad,
-                           const Segments& s, bool experts, const ExpertTPlan& p, float* Tp, bf16_t* T, int tparts,
-                           hipStream_t st) {
-  if (bf16)
-    return experts ? expert_t<bf16_t, true>((const bf16_t*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st)
-                   : expert_t<bf16_t, false>((const bf16_t*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st);
-  return experts ? expert_t<float, true>((const float*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st)
-                 : expert_t<float, false>((const float*)X, d, lowrank, lr_stride, r_pad, s, p, Tp, T, tparts, st);
+hipError_t launch_expert_prologue(const ExpertPrologue& p, bool bf16, bool packed, hipStream_t st) {
+  ExpertPrologue a = p;
+  a.nqb = (a.seg.ntok + 3) / 4;
+  if (a.d > 16384) {  // longer rows than a wave holds: a block per row
+    a.nqb = 0;
+    const hipError_t e = packed ? launch_quant_rows_fast(a.X, bf16, a.seg.ntok, a.d, a.d, 4, 4, a.xc, a.sx, nullptr, nullptr, st)
+                                : launch_quant_rows_i8(a.X, bf16, a.seg.ntok, a.d, a.d, 4, a.xc, a.sx, nullptr, nullptr, st);
+    if (e != hipSuccess) return e;
+  }
+  if (bf16) return packed ? prologue_d<bf16_t, true>(a, st) : prologue_d<bf16_t, false>(a, st);
+  return packed ? prologue_d<float, true>(a, st) : prologue_d<float, false>(a, st);
 }
 
 hipError_t launch_expert_combine(const void* Z, bool z_bf16, int n, int topk, int m, int64_t P, const int32_t* pos,

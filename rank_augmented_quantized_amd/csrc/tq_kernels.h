@@ -159,8 +159,10 @@ ProloguePlan plan_prologue(int n, int d, int r_pad, bool small, int max_chunks);
 ProloguePlan plan_prologue_fused(int n, int d, int r_pad, int max_chunks);
 // Most k-chunk partials of T the small-n GEMM sums in one pass for M tokens.
 int gemv_max_chunks(int M, int Kb, int r_pad);
+// tparts > 1: T (not its partials) in that many bf16 parts per value, rows of tparts r_pad.
 hipError_t launch_prologue(const void* X, bool bf16, int n, int d, const void* L1t, int r_pad, const ProloguePlan& p,
-                           void* xc, float* sx, float* P, void* Tout, unsigned* counters, hipStream_t st);
+                           void* xc, float* sx, float* P, void* Tout, unsigned* counters, hipStream_t st,
+                           int tparts = 0);
 // The prologue of the asymmetric layer: per-token asymmetric codes (u - 8;
 // int8 for the tile GEMM, nibble-packed for the small-n GEMM when p is a
 // small plan), scales and zero-points (zx), and T (or its k-chunk partials)

@@ -180,6 +180,7 @@ struct PrologueArgs {
   float* P;
   bf16_t* T;
   unsigned* counters;
+  int tparts;  // bf16 parts of each value of T (0 or 1: rounded once), rows of tparts r_pad
 };
 
 

@@ -343,7 +343,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_prologue(PrologueArgs a) {
   if (a.nchunk == 1) {
     for (int e = tid; e < rows * COLS; e += WAVES * 64) {
       const int rr = e / COLS, cc = e % COLS;
-      a.T[(size_t)(16 * rt + rr) * a.r_pad + col0 + cc] = (bf16_t)f32_to_bf16_bits(wave_sum(rr, cc));
+      store_t(a.T, 16 * rt + rr, a.r_pad, a.tparts, col0 + cc, wave_sum(rr, cc));
     }
     return;
   }
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_prologue(PrologueArgs a) {
       for (int k = 0; k < 8; ++k)
         if (k0 + k < nc) sum += part[k];
     }
-    a.T[(size_t)(16 * rt + rr) * a.r_pad + col0 + cc] = (bf16_t)f32_to_bf16_bits(sum);
+    store_t(a.T, 16 * rt + rr, a.r_pad, a.tparts, col0 + cc, sum);
     // chunk 0 of this element was read above by this thread only
     if (a.sum_to_p0) __hip_atomic_store(const_cast<float*>(pp), sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -550,6 +550,7 @@ struct FusedArgs {
   float* sx;
   bf16_t* T;
   float* zx;  // ASYM: per-token zero-points
+  int tparts; // bf16 parts of each value of T (0 or 1: rounded once)
 };
 constexpr int kFusedWaves = 16;
 constexpr int kFusedMaxD = 4096;  // the 16 bf16 rows fill at most 128 KiB of LDS
@@ -694,7 +695,7 @@ __global__ __launch_bounds__(1024) void k_prologue_rows(FusedArgs a) {
     float v = sP[rr * (COLS + 1) + cc];
 #pragma unroll
     for (int ww = 1; ww < WAVES; ++ww) v += sP[(ww * 16 + rr) * (COLS + 1) + cc];
-    a.T[(size_t)(row0 + rr) * a.r_pad + cc] = (bf16_t)f32_to_bf16_bits(v);
+    store_t(a.T, row0 + rr, a.r_pad, a.tparts, cc, v);
   }
 }
 
@@ -728,8 +729,9 @@ static hipError_t launch_rows_t(const FusedArgs& a, int qs, hipStream_t st) {
 }
 
 static hipError_t launch_prologue_fused(const void* X, bool bf16, int n, int d, const void* L1t, int r_pad,
-                                        void* xc, float* sx, void* Tout, hipStream_t st, float* zx = nullptr) {
-  const FusedArgs a{X, n, d, (const bf16_t*)L1t, r_pad, (uint8_t*)xc, sx, (bf16_t*)Tout, zx};
+                                        void* xc, float* sx, void* Tout, hipStream_t st, float* zx = nullptr,
+                                        int tparts = 0) {
+  const FusedArgs a{X, n, d, (const bf16_t*)L1t, r_pad, (uint8_t*)xc, sx, (bf16_t*)Tout, zx, tparts};
   const int qs = r_pad / 16;
   if (!fused_fits(d, qs)) return hipErrorInvalidValue;
   if (zx) return bf16 ? launch_rows_t<bf16_t, true>(a, qs, st) : launch_rows_t<float, true>(a, qs, st);
@@ -874,8 +876,8 @@ hipError_t launch_prologue_asym(const void* X, bool bf16, int n, int d, const vo
 }
 
 hipError_t launch_prologue(const void* X, bool bf16, int n, int d, const void* L1t, int r_pad, const ProloguePlan& p,
-                           void* xc, float* sx, float* P, void* Tout, unsigned* counters, hipStream_t st) {
-  if (p.fused) return launch_prologue_fused(X, bf16, n, d, L1t, r_pad, xc, sx, Tout, st);
+                           void* xc, float* sx, float* P, void* Tout, unsigned* counters, hipStream_t st, int tparts) {
+  if (p.fused) return launch_prologue_fused(X, bf16, n, d, L1t, r_pad, xc, sx, Tout, st, nullptr, tparts);
   if (!p.quant_in_prologue) {
     hipError_t e;
     if (p.waves == 8) {
@@ -893,7 +895,7 @@ hipError_t launch_prologue(const void* X, bool bf16, int n, int d, const void* L
     if (p.ntb == 0) return hipSuccess;
   }
   PrologueArgs a{X, n, d, (const bf16_t*)L1t, r_pad, p.kc, p.nchunk, p.qs, p.nqg, p.nqb, p.partial ? 1 : 0,
-                 p.row_blocks ? 1 : 0, p.sum_to_p0 ? 1 : 0, (uint8_t*)xc, sx, P, (bf16_t*)Tout, counters};
+                 p.row_blocks ? 1 : 0, p.sum_to_p0 ? 1 : 0, (uint8_t*)xc, sx, P, (bf16_t*)Tout, counters, tparts};
   const int ch = std::min(chunks_for(d), 32);
   return bf16 ? launch_prologue_t<bf16_t>(a, p.waves, ch, st) : launch_prologue_t<float>(a, p.waves, ch, st);
 }

@@ -8,7 +8,8 @@ from the codes' definition, and beside y a bound on |kernel - y| that arithmetic
 
 * the integer sum is exact and exact as fp32 (below 2^24); s_x s_w and its product round twice:  2 u |a|;
 * T is an fp32 sum of d exact products (gamma_d sum |x||l1|) carried in bf16 parts (2^-16 |t| with two, 2^-24 |t| with
-  three), its product with L2 an fp32 sum of parts * r_pad exact products, accumulated on top of nothing else;
+  three), its product with L2 an fp32 sum of parts * r_pad exact products, which may be accumulated on top of the
+  dequantised sum:  gamma_(parts r_pad + 2) (sum |t||l2| + |a|);
 * two more additions (low-rank term, bias):  2 u (|a| + |l| + |b|);
 * activation: slopes are at most 1.13.  exp(-w) has a relative error of |w| 2^-23 from its rounded argument; it enters
   1 / (1 + exp(-w)) with weight sigmoid(-w), and the erf form as the factor of Phi(-|v|); a reciprocal and the few
@@ -76,7 +77,7 @@ def act_rows(x, w_codes, s_w, l1=None, l2=None, bias=None, act="none", gated=Fal
         lr = t @ l2
         mag = np.abs(t) @ np.abs(l2)
         d_t = gamma(d + 16) * (np.abs(xb) @ np.abs(l1)) + (2.0 ** -16 if parts == 2 else 2.0 ** -24) * np.abs(t)
-        d_lr = d_t @ np.abs(l2) + gamma(parts * rp + 2) * (mag + d_t @ np.abs(l2))
+        d_lr = d_t @ np.abs(l2) + gamma(parts * rp + 2) * (mag + d_t @ np.abs(l2) + np.abs(a))
     b = np.zeros(a.shape[1]) if bias is None else np.asarray(bias, dtype=np.float64)
     v = a + lr + b[None, :]
     d_v = 2 * U * np.abs(a) + d_lr + 2.01 * U * (np.abs(a) + np.abs(lr) + d_lr + np.abs(b)[None, :])

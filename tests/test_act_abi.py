@@ -65,7 +65,7 @@ def _experts(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(act=9), ACT), (dict(gated=1, m=33), SHAPE), (dict(order=None), SHAPE), (dict(k=0), SHAPE), (dict(k=65), SHAPE),
-    (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(n=(1 << 23) + 1), SHAPE), (dict(n=1 << 20, k=1, d=2048), SHAPE),
+    (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(n=(1 << 23) + 1), SHAPE), (dict(n=1 << 20, k=2, d=2048), SHAPE),
     (dict(d=40), SHAPE), (dict(r=300), SHAPE), (dict(off=None), NULL), (dict(lr=None), NULL), (dict(wc=None), NULL),
     (dict(off=ODD), ALIGN), (dict(order=ODD), ALIGN), (dict(bias=ODD), ALIGN), (dict(wb=0), WS), (dict(x_dt=3), DTYPE),
     (dict(n=0), 0), (dict(E=1024, m=1 << 21), SHAPE),
