@@ -1,19 +1,32 @@
 // Tile product of the layer with its epilogue, for one layer and for experts'
-// rows (gfx950).  The main loop is the rank-augmented layer's (tq_gemm8.hip):
-// packed weight codes and int8-order activation codes go from HBM into LDS
-// by direct loads, three stages of 128 k, weights are expanded to int8 at
-// fragment read, v_mfma_i32_32x32x32_i8 accumulates exactly in int32
-// (TwinQuant notes, "TwinQuant: Learnable Subspace Decomposition for W4A4 LLM
-// Quantization", section 04.C and Figure 4).  What differs:
-//  * gated layers: a wave's 64 channels are 32 of the gate half and the same
-//    32 of the other half, so the product of the halves is taken in registers
-//    (the weight stays in its stacked layout: the rows are picked by the
-//    direct loads' addresses, a wave's loads lying all in one half);
-//  * experts: a tile's rows belong to one expert, found in a table of row
-//    tiles that the prologue wrote; token rows are gathered by the loads'
-//    addresses, which cost nothing in the loop;
-//  * the epilogue: low-rank term in two or three bf16 parts of T, bias,
-//    activation, product of the halves, residual, one store.
+// rows (gfx950): exact int32 sums of weight and activation codes on
+// v_mfma_i32_32x32x32_i8 (TwinQuant notes, "TwinQuant: Learnable Subspace
+// Decomposition for W4A4 LLM Quantization", section 04.C and Figure 4), then
+// low-rank term, bias, activation, product of a gated layer's halves and
+// residual in registers, and one store.
+//
+// A block is 4 waves and its LDS at most 80 KB, so that two blocks share a
+// compute unit: one's epilogue, barriers and load waits run under the other's
+// MFMAs.  (The rank-augmented layer's kernel, tq_gemm8.hip, has one block of
+// 8 waves per unit; with this epilogue, which is longer, every tile would
+// pay it in full.)
+//
+// Direct loads (buffer_load ... lds) bring packed weight codes, 128 k of the
+// block's channels at a time into a ring of three slots, and int8-order
+// activation codes, 64 k of its rows at a time into a ring of four; both
+// planes have 64-byte LDS rows.  One loop step is half a weight slot, 64 k:
+//   wait for the loads issued three steps ago or earlier, barrier, multiply
+//   (the weights expanded to 16 x code at fragment read), and meanwhile issue
+//   the activations of step h + 3 and half of the weights of slot h / 2 + 2
+//   into what step h - 1 freed.
+// Gated layers: a wave's 64 channels are 32 of the gate half and the same 32
+// of the other half, so their product is taken in registers; the weight stays
+// in its stacked layout, the rows are picked by the loads' addresses (a wave's
+// loads lie all in one half).  Experts: a tile's rows belong to one expert,
+// found in a table of row tiles that the prologue wrote; token rows are
+// gathered by the loads' addresses, which costs nothing in the loop.
+
+#include <type_traits>
 
 #include "tq_act.h"
 
@@ -21,29 +34,39 @@ namespace tq {
 namespace {
 
 __device__ __forceinline__ void stage_barrier() { asm volatile("s_barrier" ::: "memory"); }
-__device__ __forceinline__ int psw(int r) { return ((r >> 1) ^ (r >> 3)) & 3; }
+// LDS rows of 64 bytes: chunk c (16 bytes) of row r sits at slot c ^ psw(r).
+// A 16-byte LDS read serves 16 lanes at a time, measured to be lanes 0-3,
+// 12-15, 20-23 and 24-27 together and 4-11, 16-19 and 28-31 together (and the
+// same in the upper half): row quads {0, 3, 5, 6} and {1, 2, 4, 7}.  Rows
+// share their place modulo 256 bytes with every fourth row, so the quads of
+// each set need four different slots, which r / 4 modulo 4 gives.  (With slots
+// distinct over consecutive rows instead, every read took two passes: 5.5 M
+// of 11.1 M read cycles at 4096 x 4096 x 4096 were conflicts.)
+__device__ __forceinline__ int psw(int r) { return (r >> 2) & 3; }
 
 // vectors at any element's address (odd channel counts put rows off 16 bytes)
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
 
-// KF: code rows are whole stages, so no load needs the end-of-row test.
+// KF: code rows are whole slots (d % 128 == 0), so no load needs the
+// end-of-row test.
 template <int BM, int BN, bool GATED, bool EX, bool KF>
-__global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
-  constexpr int WGM = BM / 64, WGN = 8 / WGM;  // wave grid: channels x rows
+__global__ __launch_bounds__(256, 2) void k_tile_act(ActArgs g) {
+  constexpr int WGM = BM / 64, WGN = 4 / WGM;  // wave grid: channels x rows
   constexpr int WM = 64, WN = BN / WGN;
   constexpr int FM = 2, FN = WN / 32;
-  static_assert(WN >= 32 && (BM == 256 || BM == 128), "tile shapes");
-  constexpr int WPL = BM * 64, XPL = BN * 128, SPL = WPL + XPL;
-  constexpr int NST = 3, AHEAD = 2;
-  constexpr int WI = WPL / 1024 / 8, XI = XPL / 1024 / 8;  // direct loads per wave per stage
+  static_assert((BM == 256 || BM == 128) && WN >= 32, "tile shapes");
+  constexpr int WPL = BM * 64, XPL = BN * 64;  // one slot of each ring
+  constexpr int NWS = 3, NXS = 4, XBASE = NWS * WPL;
+  constexpr int WI = WPL / 2 / 1024 / 4, XI = XPL / 1024 / 4;  // direct loads per wave per step
   constexpr int NL = WI + XI;
   constexpr int OC = GATED ? BM / 2 : BM;  // output channels per tile
   constexpr int OW = GATED ? 32 : 64;      // per wave
+  constexpr int LDS = NWS * WPL + NXS * XPL;
   static_assert(WI >= 1 && XI >= 1, "each wave fills whole 1 KB pieces");
-  static_assert(8 * WN * OW * 2 <= NST * SPL, "Y staging fits in the stage buffers");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * SPL];
+  static_assert(4 * WN * OW * 2 <= LDS && 2 * LDS <= 160 * 1024, "Y staging fits in the rings; two blocks per unit");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WGM, wn = wave / WGM;
@@ -52,77 +75,82 @@ __global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
   const int tiles_m = (NO + OC - 1) / OC;
   int tm, tn;
   RowTile rt;
-  if (EX) {
-    // the number of row tiles is known on the device only: blocks behind the
-    // last tile leave
-    const int T = g.map[0].x * tiles_m;
+  {
+    // experts: the number of row tiles is known on the device only, and
+    // blocks behind the last tile leave
+    const int tiles_n = EX ? g.map[0].x : (g.M + BN - 1) / BN;
+    const int T = tiles_n * tiles_m;
     if ((int)blockIdx.x >= T) return;
-    const int tiles_n = g.map[0].x;
-    // regroup per XCD (any T), then walk groups of 4 channel tiles
+    // consecutive blocks go round-robin over the 8 XCDs: regroup so that each
+    // XCD has consecutive tiles, walked in groups of 4 channel tiles
     const int x = blockIdx.x & 7;
     const int b = x * (T >> 3) + min(x, T & 7) + (blockIdx.x >> 3);
     const int gsz = 4 * tiles_n, first = (b / gsz) * 4, gm = min(tiles_m - first, 4), r = b % gsz;
     tm = first + r % gm;
     tn = r / gm;
+  }
+  if (EX) {
     const int4 e = g.map[1 + tn];
     rt = RowTile{e.x, e.y, e.z};
   } else {
-    tile_of_block(blockIdx.x, tiles_m, (g.M + BN - 1) / BN, tm, tn);
     rt = RowTile{0, tn * BN, min(BN, g.M - tn * BN)};
   }
   const int o0 = tm * OC;  // first output channel
   const int Kb = g.Kb, Kx = 2 * Kb;
   const size_t wrow0 = (size_t)rt.e * g.N;
 
-  // ---- direct loads.  Load i of a wave fills 1 KB: 16 packed weight rows of
-  // 64 bytes, rows 16 (wave + 8 i) + lane / 4, or 8 activation rows of 128
-  // bytes; the XOR swizzles are applied to the fetched chunk.  Gated: LDS
-  // weight row r holds half (r / 32) % 2, output channel 32 (r / 64) + r % 32.
+  // ---- direct loads: load i of a wave fills 1 KB, 16 rows of 64 bytes, rows
+  // 16 (wave + 4 i) + lane / 4 of the plane; the XOR swizzle of the LDS rows
+  // is applied to the fetched chunk.  Gated: LDS weight row r holds half
+  // (r / 32) % 2, output channel 32 (r / 64) + r % 32.
   const int half = GATED ? (wave >> 1) & 1 : 0;
   const int wrows = min(OC, NO - o0);  // weight rows of the half (or tile) that exist
   const i32x4 rw = buffer_rsrc(g.B + (wrow0 + (size_t)half * NO + o0) * g.ldb, (uint32_t)(wrows * g.ldb));
   const bool gather = EX && g.seg.order != nullptr;
   const i32x4 rx = gather ? buffer_rsrc(g.A, (uint32_t)((int64_t)g.seg.ntok * g.lda))
                           : buffer_rsrc(g.A + (size_t)rt.row0 * g.lda, (uint32_t)(rt.rows * g.lda));
-  const int cpk = (lane & 3) ^ (((lane >> 3) ^ (2 * (wave & 1) + (lane >> 5))) & 3);
-  const int c8 = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
-  int vw[WI], vx[XI];
+  const int cpk = (lane & 3) ^ psw(16 * wave + (lane >> 2));  // 16-row pieces are 64 rows apart: one swizzle
+  int vw[2 * WI], vx[XI];
 #pragma unroll
-  for (int i = 0; i < WI; ++i) {
-    const int r = 16 * (wave + 8 * i) + (lane >> 2);
+  for (int i = 0; i < 2 * WI; ++i) {
+    const int r = 16 * (wave + 4 * i) + (lane >> 2);
     const int c = GATED ? 32 * (r >> 6) + (r & 31) : r;
     vw[i] = c < wrows ? (int)(c * g.ldb) + 16 * cpk : kOutOfRange;
   }
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
-    const int r = 8 * (wave + 8 * i) + (lane >> 3);
-    int row = r;
-    if (gather) row = row_token(g.seg, rt.row0 + min(r, rt.rows - 1));
-    vx[i] = r < rt.rows ? (int)(row * g.lda) + 16 * c8 : kOutOfRange;
+    const int r = 16 * (wave + 4 * i) + (lane >> 2);
+    const int row = gather ? row_token(g.seg, rt.row0 + min(r, rt.rows - 1)) : r;
+    vx[i] = r < rt.rows ? (int)(row * g.lda) + 16 * cpk : kOutOfRange;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
-  auto issue_one = [&](int i, int kt, int buf) {
-    const uint32_t base = lds0 + buf * SPL;
-    if (i < WI) {
-      const int sw = 64 * kt;
-      load_lds16(rw, base + 1024 * (wave + 8 * i), (KF || sw + 16 * cpk < Kb) ? vw[i] : kOutOfRange, sw);
-    } else {
-      const int sx = 128 * kt;
-      load_lds16(rx, base + WPL + 1024 * (wave + 8 * (i - WI)), (KF || sx + 16 * c8 < Kx) ? vx[i - WI] : kOutOfRange,
-                 sx);
-    }
+  const int KH = (Kx + 63) / 64, KT = (Kb + 63) / 64;
+  // part p (0, 1) of weight slot kt, and the activations of step h
+  auto issue_w = [&](int kt, int p, int slot) {
+    const int so = 64 * kt;
+    const bool ok = KF || so + 16 * cpk < Kb;
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+      load_lds16(rw, lds0 + slot * WPL + 1024 * (wave + 4 * (WI * p + i)), ok ? vw[WI * p + i] : kOutOfRange, so);
+  };
+  auto issue_x = [&](int h, int slot) {
+    const int so = 64 * h;
+    const bool ok = KF || so + 16 * cpk < Kx;
+#pragma unroll
+    for (int i = 0; i < XI; ++i)
+      load_lds16(rx, lds0 + XBASE + slot * XPL + 1024 * (wave + 4 * i), ok ? vx[i] : kOutOfRange, so);
   };
 
-  // ---- fragments: step s of a stage covers, for lane group lg, the codes of
-  // packed chunk 2 (s / 2) + lg, half s % 2, which is int8 chunk 4 (s / 2) +
-  // 2 lg + s % 2
-  int fa[2], fb[4];
+  // ---- fragments: MFMA s (0, 1) of step h takes, for lane group lg, the 16
+  // codes of half s of packed chunk 2 (h % 2) + lg, which is int8 chunk 2 lg
+  // + s of the step's activations
+  int fa[2], fb[2];
   {
     const int ra = wm * WM + l32, rb = wn * WN + l32;
 #pragma unroll
     for (int p = 0; p < 2; ++p) fa[p] = ra * 64 + 16 * ((2 * p + lg) ^ psw(ra));
 #pragma unroll
-    for (int s = 0; s < 4; ++s) fb[s] = WPL + rb * 128 + 16 * swz(4 * (s >> 1) + 2 * lg + (s & 1), rb);
+    for (int s = 0; s < 2; ++s) fb[s] = XBASE + rb * 64 + 16 * ((2 * lg + s) ^ psw(rb));
   }
   i32x16 acc[FM][FN];
 #pragma unroll
@@ -132,60 +160,53 @@ __global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0;
 
-  // multiply the stage in buffer buf; the loads of stage kn (>= 0) into
-  // buffer nb are spread over the k-steps
-  auto compute = [&](int buf, int kn, int nb) {
-    const uint8_t* s0 = smem + buf * SPL;
-    uint4 pa[2][FM];
-    i32x4 xb[2][FN];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) pa[0][f] = *reinterpret_cast<const uint4*>(s0 + fa[0] + 2048 * f);
-#pragma unroll
-    for (int f = 0; f < FN; ++f) xb[0][f] = *reinterpret_cast<const i32x4*>(s0 + fb[0] + 4096 * f);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int p = s >> 1, h = s & 1;
-      if (s == 0) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f) pa[1][f] = *reinterpret_cast<const uint4*>(s0 + fa[1] + 2048 * f);
-      }
-      if (s + 1 < 4) {
-#pragma unroll
-        for (int f = 0; f < FN; ++f) xb[(s + 1) & 1][f] = *reinterpret_cast<const i32x4*>(s0 + fb[s + 1] + 4096 * f);
-      }
-      i32x4 av[FM];
-#pragma unroll
-      for (int f = 0; f < FM; ++f)
-        av[f] = h ? unpack16(pa[p][f].z, pa[p][f].w) : unpack16(pa[p][f].x, pa[p][f].y);
-#pragma unroll
-      for (int a = 0; a < FM; ++a) {
-#pragma unroll
-        for (int b = 0; b < FN; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[a], xb[s & 1][b], acc[a][b], 0, 0, 0);
-        if (a == 0 && kn >= 0) {
-#pragma unroll
-          for (int i = NL * s / 4; i < NL * (s + 1) / 4; ++i) issue_one(i, kn, nb);
-        }
-      }
-    }
-  };
-
-  const int KT = (Kb + 63) / 64;
-#pragma unroll
-  for (int j = 0; j < AHEAD; ++j) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i)
-      if (j < KT) issue_one(i, j, j);
-  }
-  int buf = 0;
-  for (int kt = 0; kt < KT; ++kt) {
-    if (kt + AHEAD - 1 < KT)
-      wait_vmcnt<(AHEAD - 1) * NL>();
+  int ws = 0, xs = 0;  // ring slots of the current step
+  auto step = [&](int h, auto pc) {
+    constexpr int p = decltype(pc)::value;
+    // the loads of the last two steps (NL each while there are weights and
+    // activations left to fetch) may stay in flight
+    if (h + 3 < KH)
+      wait_vmcnt<2 * NL>();
     else
       wait_vmcnt<0>();
     stage_barrier();
-    compute(buf, kt + AHEAD < KT ? kt + AHEAD : -1, buf == 0 ? NST - 1 : buf - 1);
-    buf = buf == NST - 1 ? 0 : buf + 1;
+    const uint8_t* sw = smem + ws * WPL;
+    const uint8_t* sx = smem + xs * XPL;
+    uint4 pa[FM];
+    i32x4 xb[2][FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) pa[f] = *reinterpret_cast<const uint4*>(sw + fa[p] + 2048 * f);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int f = 0; f < FN; ++f) xb[s][f] = *reinterpret_cast<const i32x4*>(sx + fb[s] + 2048 * f);
+    if (h + 3 < KH) issue_x(h + 3, xs == 0 ? NXS - 1 : xs - 1);
+    if ((h >> 1) + 2 < KT) issue_w((h >> 1) + 2, p, ws == 0 ? NWS - 1 : ws - 1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      i32x4 av[FM];
+#pragma unroll
+      for (int f = 0; f < FM; ++f) av[f] = s ? unpack16(pa[f].z, pa[f].w) : unpack16(pa[f].x, pa[f].y);
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[a], xb[s][b], acc[a][b], 0, 0, 0);
+    }
+    xs = xs == NXS - 1 ? 0 : xs + 1;
+    if (p == 1) ws = ws == NWS - 1 ? 0 : ws + 1;
+  };
+  // what steps -4 .. -1 would have issued, in their order
+  issue_w(0, 0, 0);
+  issue_w(0, 1, 0);
+  issue_x(0, 0);
+  if (KH > 1) issue_x(1, 1);
+  if (KT > 1) issue_w(1, 0, 1);
+  if (KH > 2) issue_x(2, 2);
+  if (KT > 1) issue_w(1, 1, 1);
+  for (int h = 0; h < KH; h += 2) {
+    step(h, std::integral_constant<int, 0>{});
+    if (h + 1 < KH) step(h + 1, std::integral_constant<int, 1>{});
   }
 
   // ---- epilogue.  32x32 result layout: lane l, element e -> channel 8 (e / 4)
@@ -234,20 +255,36 @@ __global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
 #pragma unroll
     for (int b = 0; b < FN; ++b)
       tp[b] = g.T + ((size_t)rt.row0 + min(lrow(b), rt.rows - 1)) * g.tparts * rp + 8 * lg;
-    for (int t0 = 0; t0 < rp; t0 += 16) {
-      uint4 la[FM];
+    // step j: part j % tparts of t-range 16 (j / tparts), the last part first;
+    // DEPTH steps of operands in flight
+    constexpr int DEPTH = 3;
+    uint4 la[DEPTH][FM], tb[DEPTH][FN];
+    const int J = rp / 16 * g.tparts;
+    int lt = 0, lpart = g.tparts;  // of the next step to load
+    auto load_step = [&](uint4 (&l)[FM], uint4 (&t)[FN]) {
+      if (--lpart < 0) {
+        lpart = g.tparts - 1;
+        lt += 16;
+      }
 #pragma unroll
-      for (int a = 0; a < FM; ++a) la[a] = *reinterpret_cast<const uint4*>(lp[a] + t0);
-      for (int part = g.tparts - 1; part >= 0; --part) {
-        uint4 tb[FN];
+      for (int a = 0; a < FM; ++a) l[a] = *reinterpret_cast<const uint4*>(lp[a] + lt);
 #pragma unroll
-        for (int b = 0; b < FN; ++b) tb[b] = *reinterpret_cast<const uint4*>(tp[b] + part * rp + t0);
+      for (int b = 0; b < FN; ++b) t[b] = *reinterpret_cast<const uint4*>(tp[b] + lpart * rp + lt);
+    };
 #pragma unroll
-        for (int a = 0; a < FM; ++a)
+    for (int d = 0; d < DEPTH; ++d) load_step(la[d], tb[d]);  // J >= 4
+    for (int j = 0; j < J; j += DEPTH) {
 #pragma unroll
-          for (int b = 0; b < FN; ++b)
-            y[a][b] =
-                __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(la[a]), as_bf16x8(tb[b]), y[a][b], 0, 0, 0);
+      for (int d = 0; d < DEPTH; ++d) {
+        if (j + d < J) {
+#pragma unroll
+          for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+              y[a][b] =
+                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(la[d][a]), as_bf16x8(tb[d][b]), y[a][b], 0, 0, 0);
+          if (j + d + DEPTH < J) load_step(la[d], tb[d]);
+        }
       }
     }
   }
@@ -256,7 +293,7 @@ __global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
   // swizzled, and the 8-byte halves of a chunk swapped where bit 4 of r is
   // set, so that the 32 rows a store touches fall on distinct banks) and
   // leaves as whole 64- or 128-byte row pieces; fp32 Y is stored directly.
-  __syncthreads();  // every wave is done with the stage buffers
+  __syncthreads();  // every wave is done with the rings
   uint8_t* sY = smem + wave * (WN * OW * 2);
   auto ychunk = [&](int row, int j) { return row * (OW * 2) + 16 * (GATED ? j ^ ((row >> 2) & 3) : j ^ ((row >> 1) & 7)); };
 #pragma unroll
@@ -264,19 +301,31 @@ __global__ __launch_bounds__(512) void k_tile_act(ActArgs g) {
 #pragma unroll
     for (int e4 = 0; e4 < 4; ++e4) {
       const int c = oc(a, e4);
-      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-      const f32x4 b0 = g.bias ? load4(g.bias, 0, c) : zero;
-      const f32x4 b1 = GATED && g.bias ? load4(g.bias, 1, c) : zero;
+      f32x4 b0, b1;
+      if (g.bias) {
+        b0 = load4(g.bias, 0, c);
+        b1 = GATED ? load4(g.bias, 1, c) : b0;
+      }
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
         const int row = lrow(b);
-        float v[4];
+        float v[4], u[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = y[a][b][4 * e4 + q] + b0[q];
+        for (int q = 0; q < 4; ++q) {
+          v[q] = y[a][b][4 * e4 + q];
+          u[q] = GATED ? y[1][b][4 * e4 + q] : 1.0f;
+        }
+        if (g.bias) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] += b0[q];
+            u[q] += GATED ? b1[q] : 0.0f;
+          }
+        }
         activate4(v, g.act);
         if (GATED) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] *= y[1][b][4 * e4 + q] + b1[q];
+          for (int q = 0; q < 4; ++q) v[q] *= u[q];
         }
         const size_t o = ((size_t)rt.row0 + row) * NO + c;
         if (g.res && row < rt.rows) {
@@ -350,9 +399,9 @@ hipError_t tile_t(const ActArgs& a, hipStream_t st) {
   if (blocks <= 0 || blocks > INT32_MAX || 256 * a.ldb >= ((int64_t)1 << 31) || 256 * a.lda >= ((int64_t)1 << 31))
     return hipErrorInvalidValue;
   if (a.Kb % 64 == 0)
-    launch_kernel(k_tile_act<BM, BN, GATED, EX, true>, dim3((unsigned)blocks), dim3(512), 0, st, a);
+    launch_kernel(k_tile_act<BM, BN, GATED, EX, true>, dim3((unsigned)blocks), dim3(256), 0, st, a);
   else
-    launch_kernel(k_tile_act<BM, BN, GATED, EX, false>, dim3((unsigned)blocks), dim3(512), 0, st, a);
+    launch_kernel(k_tile_act<BM, BN, GATED, EX, false>, dim3((unsigned)blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -360,30 +409,23 @@ template <bool GATED>
 hipError_t tile_one(const ActArgs& a, hipStream_t st) {
   constexpr int OC = GATED ? 128 : 256;
   const int64_t no = GATED ? a.N / 2 : a.N, cols = (no + OC - 1) / OC;
-  // fewer 256 x 256 tiles than compute units: half as many rows, then half as
-  // many channels per tile
-  if (cols * ((a.M + 255) / 256) >= 224) return tile_t<256, 256, GATED, false>(a, st);
-  if (cols * ((a.M + 127) / 128) >= 224) return tile_t<256, 128, GATED, false>(a, st);
-  return tile_t<128, 128, GATED, false>(a, st);
+  // too few tiles for two blocks on each of the 256 compute units: half as
+  // many rows, then half as many channels per tile
+  if (cols * ((a.M + 127) / 128) >= 448) return tile_t<256, 128, GATED, false>(a, st);
+  if (cols * ((a.M + 63) / 64) >= 448) return tile_t<256, 64, GATED, false>(a, st);
+  return tile_t<128, 64, GATED, false>(a, st);
 }
 
 template <bool GATED>
 hipError_t tile_experts(const ActArgs& a, hipStream_t st) {
-  switch (tile_act_rows(a.M, a.seg.E)) {
-    case 256: return tile_t<256, 256, GATED, true>(a, st);
-    case 128: return tile_t<256, 128, GATED, true>(a, st);
-    default: return tile_t<256, 64, GATED, true>(a, st);
-  }
+  return tile_act_rows(a.M, a.seg.E) == 128 ? tile_t<256, 128, GATED, true>(a, st) : tile_t<256, 64, GATED, true>(a, st);
 }
 
 }  // namespace
 
 // By the average rows of an expert: a tile of twice as many rows would be
 // half empty, and one of half as many would read the weights twice.
-int tile_act_rows(int64_t M, int64_t E) {
-  const int64_t avg = M / E;
-  return avg > 192 ? 256 : (avg > 96 ? 128 : 64);
-}
+int tile_act_rows(int64_t M, int64_t E) { return M / E > 96 ? 128 : 64; }
 
 hipError_t launch_tile_act(const ActArgs& a, bool gated, bool experts, hipStream_t st) {
   if (experts) return gated ? tile_experts<true>(a, st) : tile_experts<false>(a, st);

@@ -137,8 +137,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, 
 }
 
 // The table of row tiles of TM rows: map[0].x = their number, map[1 + t] =
-// {expert, first row, rows, 0}.  One block of 256 threads; lds: kMaxExperts + 1
-// words and 4 more.
+// {expert, first row, rows, 0}.  One block of 256 threads; lds: kMaxExperts + 5 words.
 __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* map, int* lds) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   int* wsum = lds + kMaxExperts + 1;
@@ -182,22 +181,23 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 //  * block 0 (tile product only): the table of row tiles -- how many there
 //    are, then expert, first row and row count of each -- so that the
 //    product's blocks find their rows with one load;
-//  * blocks [nmap, nmap + nqb): codes and s_x of four tokens, one per wave
-//    (int8 order for the tile product, PK: nibble-packed for the rows product);
-//    a token is quantised once, whatever the number of its experts;
-//  * the rest: T[p] = X[token(p)] L1_e for 16 RT rows of one expert, QS
-//    16-column slices and one k-chunk, on v_mfma_f32_16x16x32_bf16 (lane l:
-//    row or column l % 16, the 8 k at 8 (l / 16)).  The four waves take the
-//    32-k steps round-robin, U of them in flight; their partials are summed
-//    through LDS in wave order, 32 columns at a time.
+//  * then T[p] = X[token(p)] L1_e for 16 RT rows of one expert, QS 16-column
+//    slices and one k-chunk, on v_mfma_f32_16x16x32_bf16 (lane l: row or
+//    column l % 16, the 8 k at 8 (l / 16)).  The four waves take the 32-k
+//    steps round-robin, U of them in flight; their partials are summed
+//    through LDS in wave order, 32 columns at a time;
+//  * the rest: codes and s_x of four tokens, one per wave (int8 order for the
+//    tile product, PK: nibble-packed for the rows product); a token is
+//    quantised once, whatever the number of its experts.  These blocks are
+//    short and fill the units beside the T blocks.
 // Few rows per expert (PK, RT = 1): L1_e is what is read (r_pad d values per
 // tile), so k is split over blocks and the partials are summed by the product
-// kernel.  Many rows (RT = 4): 64 rows share each read of L1_e and T leaves
+// kernel.  Many rows (RT = 2): 32 rows share each read of L1_e and T leaves
 // as bf16 parts.
 // ---------------------------------------------------------------------------
 template <typename XT, int CH, int RT, int QS, bool PK>
 __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
-  constexpr int U = RT == 4 ? 2 : 4, COLS = 16 * QS;
+  constexpr int U = 4, COLS = 16 * QS;
   __shared__ __attribute__((aligned(16))) float sP[4][16 * RT][33];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const Segments& s = a.seg;
@@ -211,15 +211,15 @@ __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
     }
     --b;
   }
-  if (b < a.nqb) {
-    const int row = 4 * b + w;
+  const int ntb = a.r_pad ? pl.tiles * pl.nchunk * pl.ncg : 0;
+  if (b >= ntb) {
+    const int row = 4 * (b - ntb) + w;
     if (row >= s.ntok) return;
     const float sx = quant_row_i8_wave<XT, CH, PK>((const XT*)a.X + (size_t)row * d, d >> 3, lane,
                                                    a.xc + (size_t)row * (PK ? d >> 1 : d), nullptr);
     if (lane == 0) a.sx[row] = sx;
     return;
   }
-  b -= a.nqb;
   const int lr = lane & 15, lg = lane >> 4;
   const int cg = b % pl.ncg;
   b /= pl.ncg;
@@ -387,7 +387,7 @@ hipError_t prologue_t(const ExpertPrologue& a, hipStream_t st) {
   const int64_t blocks = (a.map ? 1 : 0) + (int64_t)a.nqb + (a.r_pad ? (int64_t)a.t.tiles * a.t.nchunk * a.t.ncg : 0);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  constexpr int RT = PK ? 1 : 4;
+  constexpr int RT = PK ? 1 : 2;
   const dim3 grid((unsigned)blocks), block(256);
   if (a.t.qs == 4)
     launch_kernel(k_expert_prologue<XT, CH, RT, 4, PK>, grid, block, 0, st, a);
@@ -434,7 +434,7 @@ ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   const int nq = r_pad / 16, steps = d / 32;
   p.qs = std::min(nq, 4);
   p.ncg = nq / p.qs;
-  p.rt = partial ? 1 : 4;
+  p.rt = partial ? 1 : 2;
   p.tiles = (int)max_expert_tiles(P, E, 16 * p.rt);
   // partial: chunks of 16 steps (512 k), at most 8 of them for the product kernel to sum
   p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 8)) : 1;

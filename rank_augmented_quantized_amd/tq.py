@@ -525,7 +525,7 @@ def tq_linear_asym(X, w_codes, s_w, colsum, lowrank, m: int, r: int, y_dtype=tor
 
 
 def _need_shape(name, t, *shape):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {shape}")
 
 
@@ -540,10 +540,34 @@ def _need_elems(name, t, count):
 
 
 def _need_device(ref, *ts):
-    _need_cuda(ref, *ts)
+    """Contiguous tensors on ref's device -> that device's index."""
+    at = ref.get_device()
+    if at < 0 or not ref.is_contiguous():
+        raise ValueError("tensors must be contiguous device tensors")
     for t in ts:
-        if t is not None and t.device != ref.device:
-            raise ValueError("tensors must be on one device")
+        if t is not None:
+            if not t.is_contiguous() or not t.is_cuda:
+                raise ValueError("tensors must be contiguous device tensors")
+            if t.get_device() != at:
+                raise ValueError("tensors must be on one device")
+    return at
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, at, *args):
+    """The C entry point on the current stream of device ``at`` (a few microseconds of host time decide the smallest
+    calls, so the device is switched only when it is another one)."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == at:
+        status = fn(*args, torch.cuda.current_stream(at).cuda_stream)
+    else:
+        with torch.cuda.device(at):
+            status = fn(*args, torch.cuda.current_stream(at).cuda_stream)
+    if status != 0:
+        raise TQError(name, status)
 
 
 def linear_act_workspace(n: int, d: int, m: int, r: int, device) -> torch.Tensor:
@@ -569,8 +593,7 @@ def tq_linear_act(X, w_codes, s_w, lowrank, m: int, r: int, bias=None, act: int 
                   residual=None, y_dtype=torch.bfloat16, Y=None, ws=None):
     """Y = act(v) + residual, v = s_x s_w (Q4(X) Q4(R)) + (X L1) L2 + bias; gated: act of the first m / 2 channels
     times the others.  ``act``: TQ_ACT_*; ``residual`` may be Y."""
-    lib = load()
-    _need_device(X, w_codes, s_w, lowrank, bias, residual, Y, ws)
+    at = _need_device(X, w_codes, s_w, lowrank, bias, residual, Y, ws)
     n, d = X.shape
     mo = _layer_args(X, 1, w_codes, s_w, lowrank, m, r, bias, gated)
     if Y is None:
@@ -579,10 +602,9 @@ def tq_linear_act(X, w_codes, s_w, lowrank, m: int, r: int, bias=None, act: int 
     _need_shape("residual", residual, n, mo)
     if ws is None:
         ws = linear_act_workspace(n, d, m, r, X.device)
-    with torch.cuda.device(X.device):
-        _check("tq_linear_act", lib.tq_linear_act(
-            _p(X), _dt(X), n, d, m, r, _p(w_codes), _p(s_w), _p(lowrank), _p(bias), int(act), 1 if gated else 0,
-            _p(residual), TQ_BF16 if residual is None else _dt(residual), _p(Y), _dt(Y), _p(ws), ws.numel(), _stream(X)))
+    _call("tq_linear_act", at, X.data_ptr(), _dt(X), n, d, m, r, w_codes.data_ptr(), s_w.data_ptr(), _ptr(lowrank), _ptr(bias),
+          int(act), 1 if gated else 0, _ptr(residual), TQ_BF16 if residual is None else _dt(residual), Y.data_ptr(),
+          _dt(Y), ws.data_ptr(), ws.numel())
     return Y
 
 
@@ -594,8 +616,7 @@ def expert_plan_workspace(n: int, topk: int, E: int, device) -> torch.Tensor:
 def tq_expert_plan(ids, E: int, offsets=None, order=None, pos=None, ws=None):
     """Pairs of ids (n x topk, int32 or int64) sorted by expert -> (offsets E + 1, order n topk, pos n x topk), int32.
     Ids outside 0 .. E - 1 are dropped (pos -1)."""
-    lib = load()
-    _need_device(ids, offsets, order, pos, ws)
+    at = _need_device(ids, offsets, order, pos, ws)
     _need_dtype("ids", ids, torch.int32, torch.int64)
     n, topk = ids.shape
     if offsets is None:
@@ -611,9 +632,8 @@ def tq_expert_plan(ids, E: int, offsets=None, order=None, pos=None, ws=None):
     _need_shape("pos", pos, n, topk)
     for name, t in (("offsets", offsets), ("order", order), ("pos", pos)):
         _need_dtype(name, t, torch.int32)
-    with torch.cuda.device(ids.device):
-        _check("tq_expert_plan", lib.tq_expert_plan(_p(ids), 8 * ids.element_size(), n, topk, E, _p(offsets), _p(order),
-                                                    _p(pos), _p(ws), ws.numel(), _stream(ids)))
+    _call("tq_expert_plan", at, ids.data_ptr(), 8 * ids.element_size(), n, topk, E, offsets.data_ptr(), order.data_ptr(),
+          pos.data_ptr(), ws.data_ptr(), ws.numel())
     return offsets, order, pos
 
 
@@ -628,8 +648,7 @@ def tq_linear_experts(X, w_codes, s_w, lowrank, m: int, r: int, offsets, order=N
     """tq_linear_act on rows sorted by expert (tq_expert_plan): row p takes token order[p] // topk of X, or row p of X
     when ``order`` is None, and the weights of its expert (E stacked layers).  Rows of Y from offsets[E] on are left
     as they were (unspecified when Y is allocated here)."""
-    lib = load()
-    _need_device(X, w_codes, s_w, lowrank, offsets, order, bias, Y, ws)
+    at = _need_device(X, w_codes, s_w, lowrank, offsets, order, bias, Y, ws)
     n, d = X.shape
     E = offsets.shape[0] - 1
     mo = _layer_args(X, E, w_codes, s_w, lowrank, m, r, bias, gated)
@@ -643,17 +662,15 @@ def tq_linear_experts(X, w_codes, s_w, lowrank, m: int, r: int, offsets, order=N
     _need_shape("Y", Y, n * topk, mo)
     if ws is None:
         ws = linear_experts_workspace(n, topk, d, m, r, E, X.device)
-    with torch.cuda.device(X.device):
-        _check("tq_linear_experts", lib.tq_linear_experts(
-            _p(X), _dt(X), n, topk, d, m, r, E, _p(offsets), _p(order), _p(w_codes), _p(s_w), _p(lowrank), _p(bias),
-            int(act), 1 if gated else 0, _p(Y), _dt(Y), _p(ws), ws.numel(), _stream(X)))
+    _call("tq_linear_experts", at, X.data_ptr(), _dt(X), n, topk, d, m, r, E, offsets.data_ptr(), _ptr(order),
+          w_codes.data_ptr(), s_w.data_ptr(), _ptr(lowrank), _ptr(bias), int(act), 1 if gated else 0, Y.data_ptr(), _dt(Y),
+          ws.data_ptr(), ws.numel())
     return Y
 
 
 def tq_expert_combine(Z, pos, weights, residual=None, y_dtype=torch.bfloat16, Y=None):
     """Y[t] = residual[t] + sum_j weights[t, j] Z[pos[t, j]] (pairs with pos outside Z's rows add nothing)."""
-    lib = load()
-    _need_device(Z, pos, weights, residual, Y)
+    at = _need_device(Z, pos, weights, residual, Y)
     rows, m = Z.shape
     n, topk = pos.shape
     _need_dtype("pos", pos, torch.int32)
@@ -662,10 +679,8 @@ def tq_expert_combine(Z, pos, weights, residual=None, y_dtype=torch.bfloat16, Y=
         Y = torch.empty((n, m), dtype=y_dtype, device=Z.device)
     _need_shape("Y", Y, n, m)
     _need_shape("residual", residual, n, m)
-    with torch.cuda.device(Z.device):
-        _check("tq_expert_combine", lib.tq_expert_combine(
-            _p(Z), _dt(Z), rows, n, topk, m, _p(pos), _p(weights), _dt(weights), _p(residual),
-            TQ_BF16 if residual is None else _dt(residual), _p(Y), _dt(Y), _stream(Z)))
+    _call("tq_expert_combine", at, Z.data_ptr(), _dt(Z), rows, n, topk, m, pos.data_ptr(), weights.data_ptr(), _dt(weights),
+          _ptr(residual), TQ_BF16 if residual is None else _dt(residual), Y.data_ptr(), _dt(Y))
     return Y
 
 
