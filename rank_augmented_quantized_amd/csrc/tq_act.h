@@ -11,6 +11,7 @@ namespace tq {
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
 constexpr int kMaxExperts = 1024;
+constexpr int kRowsTile = 16;  // rows per tile of the rows kernel
 
 // Sorted rows of E experts: expert e holds rows [offsets[e], offsets[e + 1])
 // of P; row p reads token order[p] / topk (order null: token p itself).
@@ -54,7 +55,7 @@ struct ActArgs {
   void* Y;
   int y_bf16;
   Segments seg;
-  const int4* map;  // tile kernel, experts: table of row tiles
+  const int4* map;  // experts: table of row tiles, written by the prologue
 };
 
 // The tile of up to TM consecutive rows of one expert that has index t among
@@ -170,9 +171,10 @@ struct ExpertPrologue {
   int r_pad, tparts;
   Segments seg;
   ExpertTPlan t;
-  float* Tp;  // rows product: partials of T
+  float* Tp;  // partials of T
+  unsigned* counters;  // tile product with k split: one per tile and column group, zero between calls
   bf16_t* T;  // tile product: T in bf16 parts
-  int4* map;  // tile product: table of row tiles of map_rows rows
+  int4* map;  // table of row tiles of map_rows rows
   int map_rows;
   int nqb;    // set by the launcher
 };

@@ -1182,6 +1182,8 @@ struct ActWs {
 };
 // Experts with at most this many rows on average take the rows product.
 constexpr int64_t kSmallExpertRows = 8;
+// Most k-chunk partials of T that the rows product sums.
+constexpr int kMaxTChunks = 16;
 
 ActWs act_ws(int64_t n, int64_t topk, int64_t d, int64_t r, int64_t E) {
   ActWs w{};
@@ -1191,17 +1193,14 @@ ActWs act_ws(int64_t n, int64_t topk, int64_t d, int64_t r, int64_t E) {
   size_t psize = 0, msize = 0;
   if (E == 0) {
     w.plan = tq::plan_prologue((int)n, (int)d, w.r_pad, w.small,
-                               w.small ? tq::gemv_max_chunks((int)n, (int)(d / 2), w.r_pad) : 1);
+                               w.small ? kMaxTChunks : 1);
     if (w.plan.ntb > 0 && (w.plan.nchunk > 1 || w.plan.partial))
       psize = (size_t)w.plan.nchunk * (size_t)n * (size_t)w.r_pad * 4;
   } else {
     w.tplan = tq::plan_expert_t(P, (int)E, (int)d, w.r_pad, w.small);
-    if (w.small) {
-      psize = (size_t)w.tplan.nchunk * (size_t)P * (size_t)w.r_pad * 4;
-    } else {
-      w.tile_rows = tq::tile_act_rows(P, E);
-      msize = 16 * (size_t)(1 + tq::max_expert_tiles(P, E, w.tile_rows));
-    }
+    if (w.small || w.tplan.nchunk > 1) psize = (size_t)w.tplan.nchunk * (size_t)P * (size_t)w.r_pad * 4;
+    w.tile_rows = w.small ? tq::kRowsTile : tq::tile_act_rows(P, E);
+    msize = 16 * (size_t)(1 + tq::max_expert_tiles(P, E, w.tile_rows));
   }
   size_t o = tq::kSyncBytes + kCtrBytes;
   w.sx = o;
@@ -1234,7 +1233,9 @@ tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t
   const ActWs L = act_ws(n, topk, d, r, E);
   if (ws_bytes < L.total) return TQ_ERR_WORKSPACE;
   // the fixed counter region holds every counter this shape uses
-  if ((size_t)L.plan.counters * 4 > kCtrBytes) return TQ_ERR_SHAPE;
+  if ((size_t)L.plan.counters * 4 > kCtrBytes ||
+      (L.tplan.nchunk > 1 && !L.small && (size_t)L.tplan.tiles * L.tplan.ncg * 4 > kCtrBytes))
+    return TQ_ERR_SHAPE;
   uint8_t* base = (uint8_t*)ws;
   const bool xb = x_dt == TQ_BF16, ex = E > 0;
   uint8_t* xc = base + L.xc;
@@ -1281,8 +1282,9 @@ tq_status act_run(const void* X, tq_dtype x_dt, int64_t n, int64_t topk, int64_t
     p.seg = a.seg;
     p.t = L.tplan;
     p.Tp = P;
+    p.counters = (unsigned*)(base + tq::kSyncBytes);
     p.T = T;
-    p.map = L.small ? nullptr : map;
+    p.map = map;
     p.map_rows = L.tile_rows;
     TQ_RUN("experts_prologue", stream, tq::launch_expert_prologue(p, xb, L.small, stream));
   } else {

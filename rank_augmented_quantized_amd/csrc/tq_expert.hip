@@ -178,9 +178,9 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 
 // ---------------------------------------------------------------------------
 // Prologue of the experts' layers, one launch of three kinds of blocks:
-//  * block 0 (tile product only): the table of row tiles -- how many there
-//    are, then expert, first row and row count of each -- so that the
-//    product's blocks find their rows with one load;
+//  * block 0: the table of row tiles -- how many there are, then expert,
+//    first row and row count of each -- so that the product's blocks find
+//    their rows with one load;
 //  * then T[p] = X[token(p)] L1_e for 16 RT rows of one expert, QS 16-column
 //    slices and one k-chunk, on v_mfma_f32_16x16x32_bf16 (lane l: row or
 //    column l % 16, the 8 k at 8 (l / 16)).  The four waves take the 32-k
@@ -193,24 +193,23 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 // Few rows per expert (PK, RT = 1): L1_e is what is read (r_pad d values per
 // tile), so k is split over blocks and the partials are summed by the product
 // kernel.  Many rows (RT = 2): 32 rows share each read of L1_e and T leaves
-// as bf16 parts.
+// as bf16 parts, summed by the last block of a tile where k is split.
 // ---------------------------------------------------------------------------
 template <typename XT, int CH, int RT, int QS, bool PK>
 __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
   constexpr int U = 4, COLS = 16 * QS;
   __shared__ __attribute__((aligned(16))) float sP[4][16 * RT][33];
+  static_assert(sizeof(sP) >= 4 * (kMaxExperts + 5), "the table's scratch");
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const Segments& s = a.seg;
   const ExpertTPlan& pl = a.t;
   const int d = a.d;
   int b = blockIdx.x;
-  if (a.map) {
-    if (b == 0) {
-      write_tile_map(s, a.map_rows, a.map, reinterpret_cast<int*>(sP));
-      return;
-    }
-    --b;
+  if (b == 0) {
+    write_tile_map(s, a.map_rows, a.map, reinterpret_cast<int*>(sP));
+    return;
   }
+  --b;
   const int ntb = a.r_pad ? pl.tiles * pl.nchunk * pl.ncg : 0;
   if (b >= ntb) {
     const int row = 4 * (b - ntb) + w;
@@ -281,10 +280,40 @@ __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
       const int col = COLS * cg + 16 * q0 + cc;
       if (PK)
         a.Tp[((size_t)c * s.P + p) * a.r_pad + col] = v;
-      else
+      else if (pl.nchunk == 1)
         store_t(a.T, p, a.r_pad, a.tparts, col, v);
+      else  // at the device's point of coherence, for the block that sums
+        __hip_atomic_store(&a.Tp[((size_t)c * s.P + p) * a.r_pad + col], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
+  if (PK || pl.nchunk == 1) return;
+  // the last chunk's block of a tile and column group sums the partials in
+  // chunk order (every block's stores complete before it counts itself)
+  __shared__ int s_last;
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  unsigned* ctr = a.counters + t * pl.ncg + cg;
+  if (tid == 0)
+    s_last = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)pl.nchunk - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int e = tid; e < rt.rows * COLS; e += 256) {
+    const int rr = e / COLS, col = COLS * cg + e % COLS;
+    const size_t p = (size_t)rt.row0 + rr, stride = (size_t)s.P * a.r_pad;
+    const float* pp = a.Tp + p * a.r_pad + col;
+    float sum = 0.0f;
+    for (int k0 = 0; k0 < pl.nchunk; k0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = __hip_atomic_load(pp + min(k0 + k, pl.nchunk - 1) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < pl.nchunk) sum += x[k];
+    }
+    store_t(a.T, p, a.r_pad, a.tparts, col, sum);
+  }
+  if (tid == 0) __hip_atomic_store(ctr, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------------------
@@ -384,9 +413,8 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
 
 template <typename XT, int CH, bool PK>
 hipError_t prologue_t(const ExpertPrologue& a, hipStream_t st) {
-  const int64_t blocks = (a.map ? 1 : 0) + (int64_t)a.nqb + (a.r_pad ? (int64_t)a.t.tiles * a.t.nchunk * a.t.ncg : 0);
+  const int64_t blocks = 1 + (int64_t)a.nqb + (a.r_pad ? (int64_t)a.t.tiles * a.t.nchunk * a.t.ncg : 0);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  if (blocks == 0) return hipSuccess;
   constexpr int RT = PK ? 1 : 2;
   const dim3 grid((unsigned)blocks), block(256);
   if (a.t.qs == 4)
@@ -436,8 +464,14 @@ ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   p.ncg = nq / p.qs;
   p.rt = partial ? 1 : 2;
   p.tiles = (int)max_expert_tiles(P, E, 16 * p.rt);
-  // partial: chunks of 16 steps (512 k), at most 8 of them for the product kernel to sum
-  p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 8)) : 1;
+  // partial: chunks of 16 steps (512 k), at most 16 of them for the product
+  // kernel to sum.  Otherwise k is split only where there are fewer blocks
+  // than two per compute unit (64 tokens over 8 experts of d = 4096: 12 blocks
+  // of all of k took 32 us), into chunks of at least 8 steps, one per wave and
+  // batch of loads.
+  const int blocks = std::max(1, p.tiles * p.ncg);
+  p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 16))
+                     : (blocks >= 256 ? 1 : std::max(1, std::min((steps + 7) / 8, 512 / blocks)));
   p.ksteps = (steps + p.nchunk - 1) / p.nchunk;
   p.nchunk = (steps + p.ksteps - 1) / p.ksteps;
   return p;
