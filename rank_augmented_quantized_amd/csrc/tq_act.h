@@ -153,7 +153,7 @@ __device__ __forceinline__ void activate4(float (&v)[4], int act) {
 
 // Work split of the experts' first low-rank stage.
 struct ExpertTPlan {
-  int rt;      // 16-row groups per block: 1 (rows product, k-chunk partials) or 2 (tile product)
+  int rt;      // 16-row groups per block: 1 (rows product, k-chunk partials), 2 or 4 (tile product)
   int qs;      // 16-column slices per block
   int ncg;     // column groups of 16 qs
   int ksteps;  // 32-k steps per chunk

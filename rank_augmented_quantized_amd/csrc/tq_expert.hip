@@ -2,6 +2,8 @@
 // sorted by expert), the first low-rank stage of the sorted rows and the
 // weighted combination of the experts' outputs.
 
+#include <type_traits>
+
 #include "tq_act.h"
 
 namespace tq {
@@ -62,26 +64,46 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const I* ids, int64_
   for (int e = threadIdx.x; e < E; e += kPlanThreads) hist[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
-template <typename I, bool ONE>
+// ONE: the whole plan in one block.  R: rounds of 64 pairs per wave, whose ids
+// (requested at once) and matching lanes stay in registers between the two passes.
+template <typename I, bool ONE, int R>
 __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, int E, int bits, const int32_t* hist,
                                                        int32_t* offsets, int32_t* order, int32_t* pos) {
   extern __shared__ int cnt[];  // [waves][E + 1]: counts, then next positions
   __shared__ int wsum[kPlanWaves];
+  __shared__ int part[2][kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int stride = E + 1;
-  for (int i = tid; i < kPlanWaves * stride; i += kPlanThreads) cnt[i] = 0;
-  __syncthreads();
   // this wave's consecutive pairs
   const int64_t b0 = ONE ? 0 : (int64_t)blockIdx.x * kPlanChunk;
-  const int64_t blen = ONE ? P : min((int64_t)kPlanChunk, P - b0);
-  const int rounds = (int)((blen + kPlanThreads - 1) / kPlanThreads);
-  const int64_t i0 = b0 + (int64_t)w * rounds * 64;
-  const int64_t iend = b0 + blen;
+  const int64_t iend = ONE ? P : min(P, b0 + kPlanChunk);
+  const int64_t i0 = b0 + (int64_t)w * R * 64 + lane;
+  int id[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) id[r] = plan_id(ids, i0 + 64 * r, iend, E);
+  // the blocks' histograms: thread (e, g) sums every G-th block's count of expert e, all and before this block
+  const int Er = (E + 63) & ~63, G = kPlanThreads / Er, g = tid / Er, eg = tid % Er;
+  if (!ONE) {
+    int total = 0, before = 0;
+    if (g < G && eg < E) {
+#pragma unroll 16
+      for (int b = g; b < (int)gridDim.x; b += G) {
+        const int h = hist[(size_t)b * E + eg];
+        total += h;
+        before += b < (int)blockIdx.x ? h : 0;
+      }
+    }
+    part[0][tid] = total;
+    part[1][tid] = before;
+  }
+  for (int i = tid; i < kPlanWaves * stride; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
   int* my = cnt + w * stride;
-  for (int r = 0; r < rounds; ++r) {
-    const int id = plan_id(ids, i0 + 64 * r + lane, iend, E);
-    const uint64_t m = same_id(id, bits);
-    if ((m & ((1ull << lane) - 1)) == 0) my[id] += __popcll(m);  // one lane per id
+  uint64_t m[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = same_id(id[r], bits);
+    if ((m[r] & ((1ull << lane) - 1)) == 0) my[id[r]] += __popcll(m[r]);  // one lane per id
     wave_sync();
   }
   __syncthreads();
@@ -91,11 +113,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, 
     if (ONE) {
       for (int v = 0; v < kPlanWaves; ++v) total += cnt[v * stride + tid];
     } else {
-#pragma unroll 8
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int h = hist[(size_t)b * E + tid];
-        total += h;
-        before += b < (int)blockIdx.x ? h : 0;
+      for (int v = 0; v < G; ++v) {
+        total += part[0][v * Er + tid];
+        before += part[1][v * Er + tid];
       }
     }
   }
@@ -121,17 +141,17 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, 
     }
   }
   __syncthreads();
-  for (int r = 0; r < rounds; ++r) {
-    const int64_t i = i0 + 64 * r + lane;
-    const int id = plan_id(ids, i, iend, E);
-    const uint64_t m = same_id(id, bits), below = m & ((1ull << lane) - 1);
-    const int at = my[id] + __popcll(below);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = i0 + 64 * r;
+    const uint64_t below = m[r] & ((1ull << lane) - 1);
+    const int at = my[id[r]] + __popcll(below);
     wave_sync();
-    if (below == 0) my[id] = at + __popcll(m);
+    if (below == 0) my[id[r]] = at + __popcll(m[r]);
     wave_sync();
     if (i < iend) {
-      pos[i] = id < E ? at : -1;
-      if (id < E) order[at] = (int32_t)i;
+      pos[i] = id[r] < E ? at : -1;
+      if (id[r] < E) order[at] = (int32_t)i;
     }
   }
 }
@@ -183,8 +203,8 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 //    their rows with one load;
 //  * then T[p] = X[token(p)] L1_e for 16 RT rows of one expert, QS 16-column
 //    slices and one k-chunk, on v_mfma_f32_16x16x32_bf16 (lane l: row or
-//    column l % 16, the 8 k at 8 (l / 16)).  The four waves take the 32-k
-//    steps round-robin, U of them in flight; their partials are summed
+//    column l % 16, the 8 k at 8 (l / 16)).  The four waves take pairs
+//    of 32-k steps round-robin, U steps in flight; their partials are summed
 //    through LDS in wave order, 32 columns at a time;
 //  * the rest: codes and s_x of four tokens, one per wave (int8 order for the
 //    tile product, PK: nibble-packed for the rows product); a token is
@@ -192,12 +212,14 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 //    short and fill the units beside the T blocks.
 // Few rows per expert (PK, RT = 1): L1_e is what is read (r_pad d values per
 // tile), so k is split over blocks and the partials are summed by the product
-// kernel.  Many rows (RT = 2): 32 rows share each read of L1_e and T leaves
-// as bf16 parts, summed by the last block of a tile where k is split.
+// kernel.  Many rows (RT = 2 or 4): 32 or 64 rows share each read of L1_e and
+// T leaves as bf16 parts, summed by the last block of a tile where k is split.
+// Bound by the vector cache: a fragment load takes 64 bytes from each of 16
+// rows, about 5.5 TB/s over all units whatever is in flight.
 // ---------------------------------------------------------------------------
 template <typename XT, int CH, int RT, int QS, bool PK>
 __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
-  constexpr int U = 4, COLS = 16 * QS;
+  constexpr int U = 2, COLS = 16 * QS;
   __shared__ __attribute__((aligned(16))) float sP[4][16 * RT][33];
   static_assert(sizeof(sP) >= 4 * (kMaxExperts + 5), "the table's scratch");
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -238,29 +260,41 @@ __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int q = 0; q < QS; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int sb = s0 + w; sb < s1; sb += 4 * U) {
-    uint4 xa[U][RT], lb[U][QS];
+  // a wave takes pairs of steps (128 bytes of each row: whole lines); the next
+  // pairs are requested before the MFMAs of these
+  uint4 xa[2][U][RT], lb[2][U][QS];
+  auto load = [&](int sb, uint4 (&x)[U][RT], uint4 (&l)[U][QS]) {
+    auto k_of = [&](int u) { return 32 * min(sb + 8 * (u >> 1) + (u & 1), s1 - 1); };  // clamped: masked below
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = 32 * min(sb + 4 * u, s1 - 1);  // clamped: masked below
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
+      for (int u = 0; u < U; ++u) {
         float v[8];
-        Load8<XT>::load(xr[i] + k, v, xa[u][i]);
+        Load8<XT>::load(xr[i] + k_of(u), v, x[u][i]);
       }
 #pragma unroll
-      for (int q = 0; q < QS; ++q) lb[u][q] = *reinterpret_cast<const uint4*>(lp + (size_t)16 * q * d + k);
-    }
+    for (int q = 0; q < QS; ++q)
+#pragma unroll
+      for (int u = 0; u < U; ++u) l[u][q] = *reinterpret_cast<const uint4*>(lp + (size_t)16 * q * d + k_of(u));
+  };
+  auto mma = [&](int sb, const uint4 (&x)[U][RT], const uint4 (&l)[U][QS]) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (sb + 4 * u < s1) {
+      if (sb + 8 * (u >> 1) + (u & 1) < s1) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int q = 0; q < QS; ++q)
-            acc[i][q] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xa[u][i]), as_bf16x8(lb[u][q]), acc[i][q], 0, 0, 0);
+            acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u][i]), as_bf16x8(l[u][q]), acc[i][q], 0, 0, 0);
       }
+  };
+  const int sb0 = s0 + 2 * w;
+  if (sb0 < s1) load(sb0, xa[0], lb[0]);
+  for (int sb = sb0; sb < s1; sb += 8 * U) {
+    if (sb + 4 * U < s1) load(sb + 4 * U, xa[1], lb[1]);
+    mma(sb, xa[0], lb[0]);
+    if (sb + 8 * U < s1) load(sb + 8 * U, xa[0], lb[0]);
+    if (sb + 4 * U < s1) mma(sb + 4 * U, xa[1], lb[1]);
   }
 #pragma unroll
   for (int q0 = 0; q0 < QS; q0 += 2) {
@@ -398,16 +432,20 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
   int bits = 1;
   while ((1 << bits) <= E) ++bits;  // ids 0 .. E
   const unsigned lds = (unsigned)(kPlanWaves * (E + 1) * 4);
-  if (P <= kPlanOne) {
-    launch_kernel(k_plan<I, true>, dim3(1), dim3(kPlanThreads), lds, st, ids, P, E, bits, (const int32_t*)nullptr, offsets,
-                  order, pos);
+  auto one = [&](auto rc) {
+    launch_kernel(k_plan<I, true, decltype(rc)::value>, dim3(1), dim3(kPlanThreads), lds, st, ids, P, E, bits,
+                  (const int32_t*)nullptr, offsets, order, pos);
     return hipGetLastError();
-  }
+  };
+  if (P <= kPlanThreads) return one(std::integral_constant<int, 1>{});
+  if (P <= 2 * kPlanThreads) return one(std::integral_constant<int, 2>{});
+  if (P <= 4 * kPlanThreads) return one(std::integral_constant<int, 4>{});
+  if (P <= kPlanOne) return one(std::integral_constant<int, kPlanOne / kPlanThreads>{});
   const unsigned blocks = (unsigned)((P + kPlanChunk - 1) / kPlanChunk);
   launch_kernel(k_plan_hist<I>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, P, E, (int32_t*)ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  launch_kernel(k_plan<I, false>, dim3(blocks), dim3(kPlanThreads), lds, st, ids, P, E, bits, (const int32_t*)ws, offsets,
-                order, pos);
+  launch_kernel(k_plan<I, false, kPlanChunk / kPlanThreads>, dim3(blocks), dim3(kPlanThreads), lds, st, ids, P, E, bits,
+                (const int32_t*)ws, offsets, order, pos);
   return hipGetLastError();
 }
 
@@ -415,12 +453,23 @@ template <typename XT, int CH, bool PK>
 hipError_t prologue_t(const ExpertPrologue& a, hipStream_t st) {
   const int64_t blocks = 1 + (int64_t)a.nqb + (a.r_pad ? (int64_t)a.t.tiles * a.t.nchunk * a.t.ncg : 0);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  constexpr int RT = PK ? 1 : 2;
   const dim3 grid((unsigned)blocks), block(256);
-  if (a.t.qs == 4)
-    launch_kernel(k_expert_prologue<XT, CH, RT, 4, PK>, grid, block, 0, st, a);
-  else
-    launch_kernel(k_expert_prologue<XT, CH, RT, 2, PK>, grid, block, 0, st, a);
+  if constexpr (PK) {
+    if (a.t.qs == 4)
+      launch_kernel(k_expert_prologue<XT, CH, 1, 4, PK>, grid, block, 0, st, a);
+    else
+      launch_kernel(k_expert_prologue<XT, CH, 1, 2, PK>, grid, block, 0, st, a);
+  } else if (a.t.rt == 4) {
+    if (a.t.qs == 4)
+      launch_kernel(k_expert_prologue<XT, CH, 4, 4, PK>, grid, block, 0, st, a);
+    else
+      launch_kernel(k_expert_prologue<XT, CH, 4, 2, PK>, grid, block, 0, st, a);
+  } else {
+    if (a.t.qs == 4)
+      launch_kernel(k_expert_prologue<XT, CH, 2, 4, PK>, grid, block, 0, st, a);
+    else
+      launch_kernel(k_expert_prologue<XT, CH, 2, 2, PK>, grid, block, 0, st, a);
+  }
   return hipGetLastError();
 }
 
@@ -462,7 +511,9 @@ ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   const int nq = r_pad / 16, steps = d / 32;
   p.qs = std::min(nq, 4);
   p.ncg = nq / p.qs;
-  p.rt = partial ? 1 : 2;
+  // 64 rows per read of L1 where experts have that many (8192 rows over 8
+  // experts of d = 4096, r = 64: 39 us against 48 with 32 rows), else 32
+  p.rt = partial ? 1 : (P / E >= 48 ? 4 : 2);
   p.tiles = (int)max_expert_tiles(P, E, 16 * p.rt);
   // partial: chunks of 16 steps (512 k), at most 16 of them for the product
   // kernel to sum.  Otherwise k is split only where there are fewer blocks
@@ -472,7 +523,7 @@ ExpertTPlan plan_expert_t(int64_t P, int E, int d, int r_pad, bool partial) {
   const int blocks = std::max(1, p.tiles * p.ncg);
   p.nchunk = partial ? std::max(1, std::min((steps + 15) / 16, 16))
                      : (blocks >= 256 ? 1 : std::max(1, std::min((steps + 7) / 8, 512 / blocks)));
-  p.ksteps = (steps + p.nchunk - 1) / p.nchunk;
+  p.ksteps = ((steps + p.nchunk - 1) / p.nchunk + 1) & ~1;  // whole pairs
   p.nchunk = (steps + p.ksteps - 1) / p.ksteps;
   return p;
 }
