@@ -19,13 +19,15 @@ namespace {
 // ballots over the id's bits (lanes with an equal id); its counts per expert
 // in LDS carry the rank across its rounds, and sums over the waves in wave
 // order carry it across the block.
-// A block of 16 waves takes kPlanChunk pairs.  Up to kPlanOne pairs the
+// A block of 16 waves takes 2048 or 16384 pairs.  Up to kPlanOne pairs the
 // whole plan is one block and one launch; more take two launches: the blocks'
 // histograms, then each block sums the histograms of the blocks before it.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanChunk = 2048;
 constexpr int kPlanOne = 8192;
+// pairs per block beyond that: every block reads the histograms of all, so
+// many pairs take blocks of more
+constexpr int plan_chunk(int64_t P) { return P <= (1 << 18) ? 2 * kPlanThreads : 16 * kPlanThreads; }
 
 // id of pair i as an expert index, or E when dropped
 template <typename I>
@@ -54,12 +56,12 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 template <typename I>
-__global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const I* ids, int64_t P, int E, int32_t* hist) {
+__global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const I* ids, int64_t P, int E, int chunk, int32_t* hist) {
   __shared__ int cnt[kMaxExperts + 1];
   for (int e = threadIdx.x; e <= E; e += kPlanThreads) cnt[e] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kPlanChunk;
-  for (int j = threadIdx.x; j < kPlanChunk; j += kPlanThreads) atomicAdd(&cnt[plan_id(ids, i0 + j, P, E)], 1);
+  const int64_t i0 = (int64_t)blockIdx.x * chunk;
+  for (int j = threadIdx.x; j < chunk; j += kPlanThreads) atomicAdd(&cnt[plan_id(ids, i0 + j, P, E)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kPlanThreads) hist[(size_t)blockIdx.x * E + e] = cnt[e];
 }
@@ -75,8 +77,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const I* ids, int64_t P, 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int stride = E + 1;
   // this wave's consecutive pairs
-  const int64_t b0 = ONE ? 0 : (int64_t)blockIdx.x * kPlanChunk;
-  const int64_t iend = ONE ? P : min(P, b0 + kPlanChunk);
+  const int64_t b0 = ONE ? 0 : (int64_t)blockIdx.x * (R * kPlanThreads);
+  const int64_t iend = ONE ? P : min(P, b0 + R * kPlanThreads);
   const int64_t i0 = b0 + (int64_t)w * R * 64 + lane;
   int id[R];
 #pragma unroll
@@ -441,12 +443,16 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
   if (P <= 2 * kPlanThreads) return one(std::integral_constant<int, 2>{});
   if (P <= 4 * kPlanThreads) return one(std::integral_constant<int, 4>{});
   if (P <= kPlanOne) return one(std::integral_constant<int, kPlanOne / kPlanThreads>{});
-  const unsigned blocks = (unsigned)((P + kPlanChunk - 1) / kPlanChunk);
-  launch_kernel(k_plan_hist<I>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, P, E, (int32_t*)ws);
+  const int chunk = plan_chunk(P);
+  const unsigned blocks = (unsigned)((P + chunk - 1) / chunk);
+  launch_kernel(k_plan_hist<I>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, P, E, chunk, (int32_t*)ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  launch_kernel(k_plan<I, false, kPlanChunk / kPlanThreads>, dim3(blocks), dim3(kPlanThreads), lds, st, ids, P, E, bits,
-                (const int32_t*)ws, offsets, order, pos);
-  return hipGetLastError();
+  auto many = [&](auto rc) {
+    launch_kernel(k_plan<I, false, decltype(rc)::value>, dim3(blocks), dim3(kPlanThreads), lds, st, ids, P, E, bits,
+                  (const int32_t*)ws, offsets, order, pos);
+    return hipGetLastError();
+  };
+  return chunk == 2 * kPlanThreads ? many(std::integral_constant<int, 2>{}) : many(std::integral_constant<int, 16>{});
 }
 
 template <typename XT, int CH, bool PK>
@@ -496,7 +502,7 @@ hipError_t combine_t(const void* Z, int n, int topk, int m, int P, const int32_t
 }  // namespace
 
 size_t expert_plan_ws_bytes(int64_t P, int E) {
-  return P <= kPlanOne ? 0 : (size_t)((P + kPlanChunk - 1) / kPlanChunk) * (size_t)E * 4;
+  return P <= kPlanOne ? 0 : (size_t)((P + plan_chunk(P) - 1) / plan_chunk(P)) * (size_t)E * 4;
 }
 
 hipError_t launch_expert_plan(const void* ids, bool i64, int64_t P, int E, int32_t* offsets, int32_t* order,
