@@ -67,31 +67,38 @@ struct RowTile {
 };
 template <int TM>
 __device__ __forceinline__ RowTile expert_tile(const Segments& s, int t) {
+  constexpr int R = 4;  // offsets of 4 x 64 experts in flight
   const int lane = threadIdx.x & 63;
   int base = 0;
-  for (int e0 = 0; e0 < s.E; e0 += 64) {
-    const int e = e0 + lane;
-    int a = 0, b = 0;
-    if (e < s.E) {
-      a = min(max(s.offsets[e], 0), s.P);
-      b = min(max(s.offsets[e + 1], a), s.P);
-    }
-    const int tiles = (b - a + TM - 1) / TM;
-    int inc = tiles;  // inclusive sum over the lanes
+  for (int e0 = 0; e0 < s.E; e0 += 64 * R) {
+    int a[R], b[R];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(inc, d);
-      if (lane >= d) inc += y;
+    for (int r = 0; r < R; ++r) {
+      const int e = min(e0 + 64 * r + lane, s.E - 1);
+      a[r] = s.offsets[e];
+      b[r] = s.offsets[e + 1];
     }
-    const int total = __builtin_amdgcn_readlane(inc, 63);
-    if (t < base + total) {
-      const uint64_t past = __ballot(base + inc > t);  // lanes whose tiles end behind t
-      const int l = __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(past));
-      const int j = t - base - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(tiles, l));
-      const int ra = __builtin_amdgcn_readlane(a, l), rb = __builtin_amdgcn_readlane(b, l);
-      return RowTile{e0 + l, ra + j * TM, min(TM, rb - ra - j * TM)};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      a[r] = min(max(a[r], 0), s.P);
+      b[r] = min(max(b[r], a[r]), s.P);
+      const int tiles = e0 + 64 * r + lane < s.E ? (b[r] - a[r] + TM - 1) / TM : 0;
+      int inc = tiles;  // inclusive sum over the lanes
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(inc, d);
+        if (lane >= d) inc += y;
+      }
+      const int total = __builtin_amdgcn_readlane(inc, 63);
+      if (t < base + total) {
+        const uint64_t past = __ballot(base + inc > t);  // lanes whose tiles end behind t
+        const int l = __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(past));
+        const int j = t - base - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(tiles, l));
+        const int ra = __builtin_amdgcn_readlane(a[r], l), rb = __builtin_amdgcn_readlane(b[r], l);
+        return RowTile{e0 + 64 * r + l, ra + j * TM, min(TM, rb - ra - j * TM)};
+      }
+      base += total;
     }
-    base += total;
   }
   return RowTile{0, 0, 0};
 }

@@ -515,11 +515,16 @@ __global__ __launch_bounds__(64 * (NS + 2), NS == 4 ? 2 : 1) void k_stream_act(A
   }
 }
 
+template <int NS, int GB, bool GATED, int R>
+unsigned stream_lds(const ActArgs& a) {
+  constexpr int NG = GATED ? 2 * GB : GB;
+  return NS * R * NG * 16 * kPiece + NS * NG * 1024 + kItemsAhead * item_bytes(NG, a.r_pad) + 32 * a.tparts * a.r_pad;
+}
+
 template <int NS, int PW, int GB, bool GATED, bool EX, int R>
 hipError_t stream_t(const ActArgs& a, hipStream_t st) {
-  constexpr int NG = GATED ? 2 * GB : GB;
-  const unsigned lds = NS * R * NG * 16 * kPiece + NS * NG * 1024 + kItemsAhead * item_bytes(NG, a.r_pad) + 32 * a.tparts * a.r_pad;
-  if ((int64_t)16 * GB * a.ldb >= ((int64_t)1 << 31) || a.Kb > kPiece * NS * PW || lds > 160 * 1024) return hipErrorInvalidValue;
+  const unsigned lds = stream_lds<NS, GB, GATED, R>(a);
+  if (a.Kb > kPiece * NS * PW || lds > 160 * 1024) return hipErrorInvalidValue;
   const int64_t no = GATED ? a.N / 2 : a.N, ngi = (no + 16 * GB - 1) / (16 * GB);
   const int64_t items = ngi * (EX ? max_expert_tiles(a.M, a.seg.E, kRowsTile) : (a.M + 15) / 16);
   const unsigned blocks = (unsigned)std::min<int64_t>(items, NS == 4 ? 512 : 256);  // two or one per compute unit
@@ -546,7 +551,9 @@ template <bool GATED, bool EX>
 hipError_t rows_e(const ActArgs& a, hipStream_t st) {
   constexpr int SGB = GATED ? 1 : 2, RGB = GATED ? 2 : 4;
   if (a.Kb >= 1024 && a.Kb <= 2048) return stream_t<4, 4, SGB, GATED, EX, 3>(a, st);
-  if (a.Kb > 2048 && a.Kb <= 8192) return stream_t<8, 8, SGB, GATED, EX, 3>(a, st);
+  // (ranks above 128 leave no room for 8 waves' rings)
+  if (a.Kb > 2048 && a.Kb <= 8192 && stream_lds<8, SGB, GATED, 3>(a) <= 160 * 1024)
+    return stream_t<8, 8, SGB, GATED, EX, 3>(a, st);
   return rows_t<RGB, GATED, EX, 2>(a, st);
 }
 

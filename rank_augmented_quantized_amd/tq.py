@@ -539,6 +539,17 @@ def _need_elems(name, t, count):
         raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, expected at least {count}")
 
 
+def _need_place(name, t, Y):
+    """t is Y itself or lies elsewhere."""
+    if t is None:
+        return
+    a, b = t.data_ptr(), Y.data_ptr()
+    if a == b and t.dtype == Y.dtype:
+        return
+    if a < b + Y.numel() * Y.element_size() and b < a + t.numel() * t.element_size():
+        raise ValueError(f"{name} overlaps Y without being Y")
+
+
 def _need_device(ref, *ts):
     """Contiguous tensors on ref's device -> that device's index."""
     at = ref.get_device()
@@ -557,15 +568,22 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(at):
+    return torch.cuda.current_stream(at).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)  # the same without building a Stream
+
+
 def _call(name, at, *args):
     """The C entry point on the current stream of device ``at`` (a few microseconds of host time decide the smallest
     calls, so the device is switched only when it is another one)."""
     fn = getattr(load(), name)
     if torch.cuda.current_device() == at:
-        status = fn(*args, torch.cuda.current_stream(at).cuda_stream)
+        status = fn(*args, _raw_stream(at))
     else:
         with torch.cuda.device(at):
-            status = fn(*args, torch.cuda.current_stream(at).cuda_stream)
+            status = fn(*args, _raw_stream(at))
     if status != 0:
         raise TQError(name, status)
 
@@ -600,6 +618,7 @@ def tq_linear_act(X, w_codes, s_w, lowrank, m: int, r: int, bias=None, act: int 
         Y = torch.empty((n, mo), dtype=y_dtype, device=X.device)
     _need_shape("Y", Y, n, mo)
     _need_shape("residual", residual, n, mo)
+    _need_place("residual", residual, Y)
     if ws is None:
         ws = linear_act_workspace(n, d, m, r, X.device)
     _call("tq_linear_act", at, X.data_ptr(), _dt(X), n, d, m, r, w_codes.data_ptr(), s_w.data_ptr(), _ptr(lowrank), _ptr(bias),
@@ -679,6 +698,7 @@ def tq_expert_combine(Z, pos, weights, residual=None, y_dtype=torch.bfloat16, Y=
         Y = torch.empty((n, m), dtype=y_dtype, device=Z.device)
     _need_shape("Y", Y, n, m)
     _need_shape("residual", residual, n, m)
+    _need_place("residual", residual, Y)
     _call("tq_expert_combine", at, Z.data_ptr(), _dt(Z), rows, n, topk, m, pos.data_ptr(), weights.data_ptr(), _dt(weights),
           _ptr(residual), TQ_BF16 if residual is None else _dt(residual), Y.data_ptr(), _dt(Y))
     return Y

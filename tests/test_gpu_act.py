@@ -71,6 +71,21 @@ CASES = [
     (300, 2080, 640, 64, "f32", "f32", "none", False, True, "bf16"),
     (1030, 512, 514, 32, "bf16", "f32", "silu", True, False, None),
     (1100, 4096, 260, 200, "bf16", "bf16", "none", False, False, "bf16"),
+    # few rows: every kernel by row length, the longest rows, all ranks
+    (2, 16416, 40, 32, "bf16", "f32", "silu", True, True, "f32"),
+    (3, 65536, 24, 200, "bf16", "bf16", "none", False, True, None),
+    (8, 14336, 77, 64, "f32", "f32", "gelu_tanh", False, True, "f32"),
+    (9, 5120, 66, 200, "bf16", "f32", "relu", True, True, "bf16"),
+    (20, 3968, 130, 256, "bf16", "f32", "none", False, False, None),
+    (12, 2048, 5000, 0, "bf16", "bf16", "silu", True, False, None),
+    # many rows: 256 x 256 and 256 x 128 tiles, whole and ragged, each residual and its absence
+    (40, 64, 57400, 16, "bf16", "bf16", "silu", False, True, "bf16"),
+    (270, 160, 57344, 32, "bf16", "bf16", "none", False, False, "bf16"),
+    (70, 96, 57402, 40, "f32", "f32", "silu", True, True, "f32"),
+    (33, 288, 57600, 64, "bf16", "bf16", "silu", True, False, "bf16"),
+    (200, 96, 28700, 100, "bf16", "f32", "relu", False, True, "f32"),
+    (129, 512, 28672, 32, "bf16", "bf16", "silu", True, True, None),
+    (250, 64, 28673, 8, "bf16", "bf16", "none", False, True, "bf16"),
 ]
 
 
@@ -114,15 +129,51 @@ def test_no_epilogue_equals_the_plain_layer():
         assert torch.equal(out, plain), n
 
 
-@pytest.mark.parametrize("n", [2, 20, 40, 300])
+@pytest.mark.parametrize("n,d,m", [(2, 512, 390), (20, 512, 390), (20, 2048, 390), (40, 512, 390), (300, 512, 390), (40, 64, 28702), (300, 64, 57344)])
+@pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_residual_in_place(n, dt):
-    args = make(n, 512, 390, 32, 13, "bf16", True, dt, False)
-    want = call(*args, "gelu", False, dt)
+def test_residual_in_place(n, d, m, gated, dt):
+    args = make(n, d, m, 32, 13, "bf16", True, dt, gated)
+    want = call(*args, "gelu", gated, dt)
     Y = args[6].to(DEV).clone()
     lr = tq.tq_pack_lowrank(args[3].to(DEV), args[4].to(DEV))
-    tq.tq_linear_act(args[0].to(DEV), args[1].to(DEV), args[2].to(DEV), lr, 390, 32, bias=args[5].to(DEV), act=ACTS["gelu"], residual=Y, Y=Y)
+    tq.tq_linear_act(args[0].to(DEV), args[1].to(DEV), args[2].to(DEV), lr, m, 32, bias=args[5].to(DEV), act=ACTS["gelu"], gated=gated, residual=Y, Y=Y)
     assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("n,d,m,r", [(1, 2048, 96, 32), (5, 512, 99, 8), (40, 512, 99, 0), (70, 64, 57400, 16)])
+def test_nothing_is_written_beside_y(n, d, m, r):
+    args = make(n, d, m, r, 23, "bf16", True, None, False)
+    for y in ("bf16", "f32"):
+        guard = torch.full((n + 32, m), 5.0, dtype=DT[y], device=DEV)
+        off = 16  # rows, a multiple of 16 bytes for every m
+        call(*args, "silu", False, y, Y=guard[off: off + n])
+        torch.cuda.synchronize()
+        assert (guard[:off] == 5.0).all() and (guard[off + n:] == 5.0).all()
+        assert_within(guard[off: off + n].float().cpu().numpy(), *reference(*args, "silu", False, y), what=y)
+
+
+def test_no_rows():
+    X = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    out = tq.tq_linear_act(X, torch.zeros((32, 32), dtype=torch.uint8, device=DEV), torch.ones(32, device=DEV), None, 32, 0)
+    assert out.shape == (0, 32)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight on two streams, each with its own workspace."""
+    a, b = make(64, 2048, 1024, 32, 5, "bf16", True, None, False), make(3, 4096, 2048, 64, 6, "bf16", True, None, True)
+    want = [call(*a, "silu", False, "f32"), call(*b, "gelu", True, "f32")]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(6):
+        with torch.cuda.stream(s1):
+            got[0].append(call(*a, "silu", False, "f32"))
+        with torch.cuda.stream(s2):
+            got[1].append(call(*b, "gelu", True, "f32"))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
 
 
 def test_one_workspace_for_every_shape():
@@ -188,6 +239,9 @@ def test_binding_refuses_wrong_shapes():
     for bad in (dict(bias=b[:31]), dict(residual=rs[:3]), dict(Y=torch.empty((4, 16), dtype=torch.bfloat16, device=DEV)), dict(bias=b.half())):
         with pytest.raises((ValueError, TypeError)):
             tq.tq_linear_act(X, codes, s_w, lr, 32, 8, **{**ok, **bad})
+    both = torch.zeros((5, 32), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):  # overlapping, not the same
+        tq.tq_linear_act(X, codes, s_w, lr, 32, 8, residual=both[:4], Y=both[1:])
     with pytest.raises(ValueError):
         tq.tq_linear_act(X, codes[:30], s_w, lr, 32, 8)
     with pytest.raises(ValueError):

@@ -126,6 +126,17 @@ ECASES = [
     (700, 1, 3, 1024, 300, 32, "f32", "f32", "none", False, False, "one", False),
     (900, 2, 4, 544, 520, 48, "bf16", "f32", "gelu", True, True, "mixed", True),
     (12, 2, 5, 64, 32, 8, "bf16", "bf16", "none", False, False, "none", True),
+    # few rows per expert: each kernel by row length, all ranks, many experts
+    (6, 2, 3, 16416, 20, 16, "bf16", "f32", "none", False, True, "mixed", True),
+    (5, 2, 4, 14336, 40, 64, "f32", "bf16", "silu", True, False, "dropped", False),
+    (7, 2, 4, 5120, 34, 200, "bf16", "f32", "none", False, True, "mixed", True),
+    (30, 3, 9, 2048, 130, 128, "bf16", "f32", "gelu", True, True, "dropped", True),
+    (20, 4, 1000, 64, 16, 8, "bf16", "f32", "none", False, True, "mixed", True),
+    # many: tiles of 128 and 256 rows, k split over blocks and not
+    (300, 2, 4, 256, 300, 32, "bf16", "bf16", "silu", True, True, "mixed", True),
+    (310, 2, 4, 96, 513, 0, "f32", "f32", "relu", False, True, "dropped", True),
+    (2600, 4, 9, 64, 80, 200, "bf16", "f32", "none", False, False, "mixed", True),
+    (60, 2, 2, 16416, 36, 32, "bf16", "bf16", "none", False, False, "mixed", True),
 ]
 
 
