@@ -489,10 +489,14 @@ template <bool GATED>
 hipError_t tile_one(const ActArgs& a, hipStream_t st) {
   constexpr int OC = GATED ? 128 : 256;
   const int64_t no = GATED ? a.N / 2 : a.N, cols = (no + OC - 1) / OC;
-  // fewer 256 x 256 tiles than compute units: half as many rows, then small
-  // tiles, two blocks per unit
-  if (cols * ((a.M + 255) / 256) >= 224) return tile_t<256, 256, 8, GATED, false>(a, st);
-  if (cols * ((a.M + 127) / 128) >= 224) return tile_t<256, 128, 8, GATED, false>(a, st);
+  // three quarters of the compute units must have a tile: else half as many
+  // rows, then small tiles, two blocks per unit.  d = 4096, gated, 256- against
+  // 128-row tiles: 512 tokens x 12288 (192 tiles of 256) 59.6 and 69.1 us;
+  // 2048 x 4096 ungated (128 tiles) 55.7 and 39.1.  128-row against small tiles:
+  // 256 x 14336 (224 tiles) 37.0 and 47.7; 1024 x 4096 ungated (128) 33.1 and
+  // 25.8; 128 x 14336 (112) 50.6 and 25.8.
+  if (cols * ((a.M + 255) / 256) >= 192) return tile_t<256, 256, 8, GATED, false>(a, st);
+  if (cols * ((a.M + 127) / 128) >= 192) return tile_t<256, 128, 8, GATED, false>(a, st);
   return tile_t<128, 64, 4, GATED, false>(a, st);
 }
 
@@ -507,11 +511,15 @@ hipError_t tile_experts(const ActArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// By the average rows of an expert: a tile of twice as many rows would be
-// half empty, and one of half as many would read the weights twice.
+// By the average rows of an expert: a tile of twice as many rows would be half
+// empty more often than not, and one of half as many reads the weights twice.
+// 8 experts, 4096 -> 14336 gated: 125 rows each, 221 us with 64-row tiles and
+// 208 with 128; 250 rows, 310 with 128 and 323 with 256; 500 rows, 536 with 128
+// and 506 with 256; 1024 rows, 1013 and 901.  128 experts, 2048 -> 768 gated:
+// 128 rows, 120 us with 64 and 108 with 128.
 int tile_act_rows(int64_t M, int64_t E) {
   const int64_t avg = M / E;
-  return avg > 192 ? 256 : (avg > 96 ? 128 : 64);
+  return avg > 384 ? 256 : (avg > 96 ? 128 : 64);
 }
 
 hipError_t launch_tile_act(const ActArgs& a, bool gated, bool experts, hipStream_t st) {

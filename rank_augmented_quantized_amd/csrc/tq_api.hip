@@ -1180,7 +1180,13 @@ struct ActWs {
   tq::ProloguePlan plan;    // one layer
   tq::ExpertTPlan tplan;    // experts
 };
-// Experts with at most this many rows on average take the rows product.
+// Experts with at most this many rows on average take the rows product, whose
+// prologue leaves nibble-packed codes and partials of T (both launches, rows
+// against tiles: 8 experts, 4096 -> 14336 gated, 4 rows each 98 and 119 us, 8
+// rows 129 and 132, 12 rows 135 and 131; 64 experts, 2048 -> 1024 gated, 8 rows
+// 44 and 48, 16 rows 54 and 50).  One layer takes it up to kSmallN rows as
+// tq_linear does (32 rows, 4096 -> 4096: 14.7 against 25.4 us; 4096 -> 14336
+// gated: 28 against 27).
 constexpr int64_t kSmallExpertRows = 8;
 // Most k-chunk partials of T that the rows product sums.
 constexpr int kMaxTChunks = 16;
