@@ -359,6 +359,7 @@ __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
 // columns (16 bytes of bf16) per thread and up to 8 rows in flight; the
 // token's positions and weights are the same for the whole block.
 // ---------------------------------------------------------------------------
+constexpr int kCombineTokens = 1 << 20;  // per grid layer: a launch takes fewer than 2^32 threads along x
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
@@ -372,12 +373,12 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
 }
 
 template <typename ZT, typename WT, int VEC>
-__global__ __launch_bounds__(256) void k_combine(const ZT* __restrict__ Z, int topk, int m, int P,
+__global__ __launch_bounds__(256) void k_combine(const ZT* __restrict__ Z, int n, int topk, int m, int P,
                                                  const int32_t* __restrict__ pos, const WT* __restrict__ wt,
                                                  const void* res, int res_bf16, void* Y, int y_bf16) {
-  const int t = blockIdx.x;
+  const int t = blockIdx.z * kCombineTokens + blockIdx.x;
   const int c = (blockIdx.y * 256 + threadIdx.x) * VEC;
-  if (c >= m) return;
+  if (c >= m || t >= n) return;
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
@@ -490,11 +491,12 @@ hipError_t prologue_d(const ExpertPrologue& a, hipStream_t st) {
 template <typename ZT, typename WT>
 hipError_t combine_t(const void* Z, int n, int topk, int m, int P, const int32_t* pos, const void* w, const void* res,
                      bool res_bf16, void* Y, bool y_bf16, hipStream_t st) {
+  const unsigned x = (unsigned)std::min(n, kCombineTokens), z = (unsigned)((n - 1) / kCombineTokens + 1);
   if (m % 8 == 0)
-    launch_kernel(k_combine<ZT, WT, 8>, dim3((unsigned)n, (unsigned)((m + 2047) / 2048)), dim3(256), 0, st, (const ZT*)Z, topk,
+    launch_kernel(k_combine<ZT, WT, 8>, dim3(x, (unsigned)((m + 2047) / 2048), z), dim3(256), 0, st, (const ZT*)Z, n, topk,
                   m, P, pos, (const WT*)w, res, res_bf16 ? 1 : 0, Y, y_bf16 ? 1 : 0);
   else
-    launch_kernel(k_combine<ZT, WT, 1>, dim3((unsigned)n, (unsigned)((m + 255) / 256)), dim3(256), 0, st, (const ZT*)Z, topk, m,
+    launch_kernel(k_combine<ZT, WT, 1>, dim3(x, (unsigned)((m + 255) / 256), z), dim3(256), 0, st, (const ZT*)Z, n, topk, m,
                   P, pos, (const WT*)w, res, res_bf16 ? 1 : 0, Y, y_bf16 ? 1 : 0);
   return hipGetLastError();
 }

@@ -243,6 +243,16 @@ def test_combine_in_place_and_out_of_range_positions():
     assert torch.equal(none, Y.bfloat16())
 
 
+def test_combine_of_the_most_tokens():
+    """2^24 tokens of one expert each, Y[t] = 2 Z[n - 1 - t] exactly, the last blocks' rows among them."""
+    n = 1 << 24
+    Z = torch.arange(n, dtype=torch.float32, device=DEV).view(n, 1)
+    pos = torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV).view(n, 1)
+    w = torch.full((n, 1), 2.0, device=DEV)
+    Y = tq.tq_expert_combine(Z, pos, w, y_dtype=torch.float32)
+    assert torch.equal(Y, 2 * Z.flip(0))
+
+
 def mlp(X, ids, wt, E, gu, dn, m1, m2, r, bufs=None):
     """The experts' MLP as a model calls it: plan, gate and up, down on the sorted rows, combination on the residual."""
     b = bufs or {}
@@ -305,6 +315,46 @@ def test_graph_replay_with_new_routing(n):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(bufs["Y"], eager), kind
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs of different shapes captured with one workspace and one set of outputs, replayed in turn with eager work
+    between: a launch leaves nothing in the workspace that the next one reads."""
+    E, d, m, r = 8, 2048, 96, 64
+    lay = layers(E, d, m, r, 41, True)
+    dev = (lay[0].to(DEV), lay[1].to(DEV), pack(lay[2], lay[3]), lay[4].to(DEV))
+    runs, need = [], 0
+    for n, k in ((6, 2), (150, 2), (40, 4)):  # the rows product; the tile product, T split over k
+        g = torch.Generator().manual_seed(n)
+        X = torch.randn((n, d), generator=g).bfloat16().to(DEV)
+        ids = torch.from_numpy(draw_ids(n, k, E, n, "mixed")).to(DEV)
+        plan = tq.tq_expert_plan(ids, E)
+        runs.append((X, k, plan))
+        need = max(need, tq.linear_experts_workspace(n, k, d, m, r, E, DEV).numel())
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    out = [torch.empty((X.shape[0] * k, m), dtype=torch.bfloat16, device=DEV) for X, k, _ in runs]
+
+    def once(i):
+        X, k, (offsets, order, _) = runs[i]
+        tq.tq_linear_experts(X, dev[0], dev[1], dev[2], m, r, offsets, order=order, topk=k, bias=dev[3], act=2, Y=out[i], ws=ws)
+
+    want = []
+    for i in range(3):
+        once(i)
+        want.append(out[i].clone())
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(3):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            once(i)
+        graphs.append(graph)
+    for i in (0, 1, 2, 1, 0, 2, 2, 1):
+        out[i].zero_()
+        graphs[i].replay()
+        once((i + 1) % 3)
+        torch.cuda.synchronize()
+        assert torch.equal(out[i], want[i]), i
 
 
 def test_binding_refuses_wrong_shapes():
