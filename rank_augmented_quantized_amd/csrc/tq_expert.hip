@@ -19,15 +19,22 @@ namespace {
 // ballots over the id's bits (lanes with an equal id); its counts per expert
 // in LDS carry the rank across its rounds, and sums over the waves in wave
 // order carry it across the block.
-// A block of 16 waves takes 2048 or 16384 pairs.  Up to kPlanOne pairs the
+// A block of 16 waves takes 2048 to 16384 pairs.  Up to kPlanOne pairs the
 // whole plan is one block and one launch; more take two launches: the blocks'
 // histograms, then each block sums the histograms of the blocks before it.
+// Bound by latency: 16 tokens x 8 of 128 experts 7.4 us a call, 32768 x 8 of
+// 256 11.4 us for 4.2 MB.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanOne = 8192;
-// pairs per block beyond that: every block reads the histograms of all, so
-// many pairs take blocks of more
-constexpr int plan_chunk(int64_t P) { return P <= (1 << 18) ? 2 * kPlanThreads : 16 * kPlanThreads; }
+// one block against two launches: 4096 pairs of 128 experts 6.8 and 7.3 us, 8192 pairs 11.3 and 7.6
+constexpr int kPlanOne = 4096;
+// Pairs per block beyond that.  A wave ranks its pairs one round after the
+// other, so few per block are fastest until every block's reading of all
+// blocks' histograms weighs more (2048, 4096 and 16384 pairs per block, 256
+// experts: 2^18 pairs 11.8, 14.4 and 28.3 us; 2^19 16.1, 18.1 and 29.8; 2^20
+// 37, 26 and 33; 2^22 364, 131 and 49; 2^24 5131, 1593 and 243).
+constexpr int plan_rounds(int64_t P) { return P <= (1 << 19) ? 2 : (P <= (1 << 20) ? 4 : 16); }
+constexpr int plan_chunk(int64_t P) { return plan_rounds(P) * kPlanThreads; }
 
 // id of pair i as an expert index, or E when dropped
 template <typename I>
@@ -217,7 +224,8 @@ __device__ __forceinline__ void write_tile_map(const Segments& s, int TM, int4* 
 // kernel.  Many rows (RT = 2 or 4): 32 or 64 rows share each read of L1_e and
 // T leaves as bf16 parts, summed by the last block of a tile where k is split.
 // Bound by the vector cache: a fragment load takes 64 bytes from each of 16
-// rows, about 5.5 TB/s over all units whatever is in flight.
+// rows, about 5.5 TB/s over all units whatever is in flight.  4096 tokens x 2
+// of 8 experts, d = 4096, r = 64: 40 us; 4 tokens of them 6 us.
 // ---------------------------------------------------------------------------
 template <typename XT, int CH, int RT, int QS, bool PK>
 __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
@@ -357,7 +365,8 @@ __global__ __launch_bounds__(256) void k_expert_prologue(ExpertPrologue a) {
 // of j and one rounding.  Dropped pairs (pos outside 0 .. P - 1) add nothing,
 // whatever their weight or the rows of Z hold.  Bound by reading Z: VEC
 // columns (16 bytes of bf16) per thread and up to 8 rows in flight; the
-// token's positions and weights are the same for the whole block.
+// token's positions and weights are the same for the whole block.  4095 tokens
+// x 8 of a prefill batch in bf16, 322 MB: 65 us, 4.9 TB/s, the rate of a copy.
 // ---------------------------------------------------------------------------
 constexpr int kCombineTokens = 1 << 20;  // per grid layer: a launch takes fewer than 2^32 threads along x
 template <typename T, int VEC>
@@ -442,7 +451,6 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
   };
   if (P <= kPlanThreads) return one(std::integral_constant<int, 1>{});
   if (P <= 2 * kPlanThreads) return one(std::integral_constant<int, 2>{});
-  if (P <= 4 * kPlanThreads) return one(std::integral_constant<int, 4>{});
   if (P <= kPlanOne) return one(std::integral_constant<int, kPlanOne / kPlanThreads>{});
   const int chunk = plan_chunk(P);
   const unsigned blocks = (unsigned)((P + chunk - 1) / chunk);
@@ -453,7 +461,11 @@ hipError_t plan_t(const I* ids, int64_t P, int E, int32_t* offsets, int32_t* ord
                   (const int32_t*)ws, offsets, order, pos);
     return hipGetLastError();
   };
-  return chunk == 2 * kPlanThreads ? many(std::integral_constant<int, 2>{}) : many(std::integral_constant<int, 16>{});
+  switch (plan_rounds(P)) {
+    case 2: return many(std::integral_constant<int, 2>{});
+    case 4: return many(std::integral_constant<int, 4>{});
+    default: return many(std::integral_constant<int, 16>{});
+  }
 }
 
 template <typename XT, int CH, bool PK>
@@ -503,8 +515,11 @@ hipError_t combine_t(const void* Z, int n, int topk, int m, int P, const int32_t
 
 }  // namespace
 
+// grows with P, so that a workspace for the most pairs serves fewer
 size_t expert_plan_ws_bytes(int64_t P, int E) {
-  return P <= kPlanOne ? 0 : (size_t)((P + plan_chunk(P) - 1) / plan_chunk(P)) * (size_t)E * 4;
+  if (P <= kPlanOne) return 0;
+  const int64_t blocks = (P + plan_chunk(P) - 1) / plan_chunk(P);
+  return (size_t)std::max<int64_t>(blocks, P > (1 << 19) ? 256 : 0) * (size_t)E * 4;
 }
 
 hipError_t launch_expert_plan(const void* ids, bool i64, int64_t P, int E, int32_t* offsets, int32_t* order,

@@ -105,4 +105,7 @@ def test_size_queries(lib):
     assert lib.tq_expert_plan_workspace_bytes(4, 2, 8) == 0
     assert lib.tq_expert_plan_workspace_bytes(1 << 20, 2, 8) > 0
     assert lib.tq_expert_plan_workspace_bytes(4, 2, 1025) == 0
+    sizes = [lib.tq_expert_plan_workspace_bytes(1 << b, 1, 64) for b in range(25)]  # for the most tokens: enough for fewer
+    assert sizes == sorted(sizes) and lib.tq_expert_plan_workspace_bytes((1 << 19) + 1, 1, 64) >= sizes[19]
+    assert lib.tq_expert_plan_workspace_bytes((1 << 20) + 1, 1, 64) >= sizes[20]
     assert lib.tq_status_string(-8).startswith(b"TQ_ERR_ACT")

@@ -53,6 +53,7 @@ PLANS = [(0, 2, 4, "mixed"), (1, 1, 1, "mixed"), (1, 8, 8, "mixed"), (3, 2, 1, "
          (63, 1, 64, "mixed"), (64, 1, 63, "same"), (65, 3, 1024, "mixed"), (1000, 8, 257, "dropped"), (1024, 8, 16, "one"),
          (1025, 8, 33, "mixed"), (4097, 6, 1024, "dropped"), (9001, 8, 100, "none"), (33333, 8, 256, "mixed"), (20000, 5, 3, "one"), (32768, 8, 1024, "dropped"),
          (66000, 4, 300, "mixed"), (70001, 8, 8, "dropped")]
+PLANS += [(512, 8, 40, "mixed"), (513, 8, 1000, "dropped"), (66001, 8, 130, "dropped"), (131100, 8, 1024, "mixed")]  # either side of each block size
 
 
 @pytest.mark.parametrize("bits", [32, 64])
