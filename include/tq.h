@@ -498,7 +498,8 @@ tq_status tq_linear_act(const void* X, tq_dtype x_dt, int64_t n, int64_t d, int6
  *            from offsets[E] on are left as they were.
  *   pos      out: n topk int32; sorted position of each pair, -1 if dropped.
  *   ws       tq_expert_plan_workspace_bytes(n, topk, E) bytes of scratch (0
- *            for small plans: ws may then be NULL).
+ *            for small plans: ws may then be NULL); never fewer for more
+ *            pairs, so one for the most serves all.
  * The result depends on the ids alone (no atomics decide an order).  Shapes:
  * 1 <= E <= 1024, 1 <= topk <= 64, n topk <= 2^24; n == 0 writes offsets = 0.
  * TQ_ERR_BITS for other id widths.
@@ -545,7 +546,7 @@ tq_status tq_linear_experts(const void* X, tq_dtype x_dt, int64_t n, int64_t top
  *   weights  n x topk (w_dt).
  *   residual n x m (res_dt) or NULL; it may be Y itself (same type).
  *   Y        out: n x m (y_dt).
- * 1 <= topk <= 64, 1 <= m <= 2^22; rows <= 2^24 (may be 0).
+ * 1 <= topk <= 64, n topk <= 2^24, 1 <= m <= 2^22; rows <= 2^24 (may be 0).
  */
 tq_status tq_expert_combine(const void* Z, tq_dtype z_dt, int64_t rows, int64_t n, int64_t topk, int64_t m,
                             const int32_t* pos, const void* weights, tq_dtype w_dt, const void* residual,
