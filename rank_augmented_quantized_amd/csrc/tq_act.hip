@@ -221,8 +221,9 @@ __global__ __launch_bounds__(256, 4) void k_rows_act(ActArgs g) {
 // Stream kernel: the rows kernel's work for rows of d = 2048 .. 16384, as a
 // stream that never drains.  One item is 16 GB output channels (gated: of each
 // half) of one row tile; a block takes a contiguous range of the items.
-//   * NS stream waves split K into 128-byte pieces.  A wave keeps the tile's
-//     activation codes of its pieces in registers and streams the weights
+//   * NS stream waves take 128-byte pieces of K in turn (neighbouring waves on
+//     neighbouring lines).  A wave keeps the tile's activation codes of its
+//     pieces in registers and streams the weights
 //     through its own LDS ring by direct loads, R units (one piece of all the
 //     item's rows, 8 rows of 128 contiguous bytes per load) ahead, across item
 //     and tile boundaries; it waits for its own loads only.
@@ -235,9 +236,9 @@ __global__ __launch_bounds__(256, 4) void k_rows_act(ActArgs g) {
 //     the next item streams.
 // Per item two barriers: partials and item data are there; they have been read.
 // Bound by HBM: 4 tokens x 2 of 8 experts of 4096 -> 14336 gated, r = 64, 5
-// experts active: 59.7 us, 312 MB at 5.2 TB/s (reading 1 GiB: 5.7); without
-// the loader wave 63 to 70 us.  One layer of that shape, one token, is 63 MB
-// in 17.3 us, 3.6 TB/s: starting and draining the rings is a third of it.
+// experts active: 54 us, 312 MB at 5.7 TB/s, the rate of a large read; without
+// the loader wave about a tenth more.  One layer of that shape, one token, is
+// 63 MB in 16.5 us, 3.8 TB/s: starting and draining the rings is a third of it.
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 128;  // bytes of a weight row per unit
 // chunk c (16 bytes) of LDS row r sits at slot c ^ (r / 2 modulo 8): a fragment
@@ -257,9 +258,19 @@ __device__ __forceinline__ void wait_vmcnt_upto(int n) {
   }
   wait_vmcnt<N>();
 }
+// load_lds16 with the non-temporal hint, for weights that one launch reads once
+__device__ __forceinline__ void load_lds16_nt(i32x4 rsrc, uint32_t lds, int voff, int soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0");
+}
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int NS, int PW, int GB, bool GATED, bool EX, int R>
+// ONCE: weights loaded with the non-temporal hint.
+template <int NS, int PW, int GB, bool GATED, bool EX, int R, bool ONCE>
 __global__ __launch_bounds__(64 * (NS + 2), NS == 4 ? 2 : 1) void k_stream_act(ActArgs g) {
   constexpr int H = GATED ? 2 : 1, NG = H * GB;
   constexpr int UNIT = NG * 16 * kPiece, LPU = 2 * NG;  // bytes and direct loads per unit
@@ -288,9 +299,9 @@ __global__ __launch_bounds__(64 * (NS + 2), NS == 4 ? 2 : 1) void k_stream_act(A
   const int t_first = (int)(i0 / ngi), c_first = (int)(i0 % ngi);
 
   if (wave < NS) {
-    // ---- stream wave: pieces p0 .. p0 + np - 1 ----
-    const int KP = (g.Kb + kPiece - 1) / kPiece, per = (KP + NS - 1) / NS;
-    const int p0 = wave * per, np = max(0, min(KP, p0 + per) - p0);
+    // ---- stream wave: np pieces, every NS-th from its own number on ----
+    const int KP = (g.Kb + kPiece - 1) / kPiece;
+    const int np = max(0, (KP - wave + NS - 1) / NS);
     const int units = n * np;
     const uint8_t* ringp = smem + wave * R * UNIT;
     const uint32_t ring = lds_of(ringp);
@@ -313,15 +324,19 @@ __global__ __launch_bounds__(64 * (NS + 2), NS == 4 ? 2 : 1) void k_stream_act(A
       vo[h] = (int)(r * g.ldb) + 16 * ((lane & 7) ^ ssw(r));
     }
     auto issue = [&](int slot) {
-      const int so = kPiece * (p0 + lp);
+      const int so = kPiece * (wave + NS * lp);
 #pragma unroll
       for (int q = 0; q < NG; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = 8 * h + (lane >> 3);
           const bool ok = so + 16 * ((lane & 7) ^ ssw(r)) < g.Kb;  // rows past the channels end past the resource
-          load_lds16(rsrc[q / GB], ring + slot * UNIT + q * (16 * kPiece) + h * 1024,
-                     ok ? vo[h] + (int)(16 * (q % GB) * g.ldb) : kOutOfRange, so);
+          const uint32_t at = ring + slot * UNIT + q * (16 * kPiece) + h * 1024;
+          const int off = ok ? vo[h] + (int)(16 * (q % GB) * g.ldb) : kOutOfRange;
+          if constexpr (ONCE)
+            load_lds16_nt(rsrc[q / GB], at, off, so);
+          else
+            load_lds16(rsrc[q / GB], at, off, so);
         }
       ++issued;
       if (++lp == np) {
@@ -343,7 +358,7 @@ __global__ __launch_bounds__(64 * (NS + 2), NS == 4 ? 2 : 1) void k_stream_act(A
       for (int p = 0; p < PW; ++p)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int k = kPiece * (p0 + p) + 64 * s + 16 * lg;
+          const int k = kPiece * (wave + NS * p) + 64 * s + 16 * lg;
           av[p][s] = *reinterpret_cast<const uint4*>(ap + min(k, g.Kb - 16));
           if (p >= np || k >= g.Kb) av[p][s] = uint4{0, 0, 0, 0};
         }
@@ -528,14 +543,14 @@ unsigned stream_lds(const ActArgs& a) {
   return NS * R * NG * 16 * kPiece + NS * NG * 1024 + kItemsAhead * item_bytes(NG, a.r_pad) + 32 * a.tparts * a.r_pad;
 }
 
-template <int NS, int PW, int GB, bool GATED, bool EX, int R>
+template <int NS, int PW, int GB, bool GATED, bool EX, int R, bool ONCE>
 hipError_t stream_t(const ActArgs& a, hipStream_t st) {
   const unsigned lds = stream_lds<NS, GB, GATED, R>(a);
   if (a.Kb > kPiece * NS * PW || lds > 160 * 1024) return hipErrorInvalidValue;
   const int64_t no = GATED ? a.N / 2 : a.N, ngi = (no + 16 * GB - 1) / (16 * GB);
   const int64_t items = ngi * (EX ? max_expert_tiles(a.M, a.seg.E, kRowsTile) : (a.M + 15) / 16);
   const unsigned blocks = (unsigned)std::min<int64_t>(items, NS == 4 ? 512 : 256);  // two or one per compute unit
-  launch_kernel(k_stream_act<NS, PW, GB, GATED, EX, R>, dim3(blocks), dim3(64 * (NS + 2)), lds, st, a);
+  launch_kernel(k_stream_act<NS, PW, GB, GATED, EX, R, ONCE>, dim3(blocks), dim3(64 * (NS + 2)), lds, st, a);
   return hipGetLastError();
 }
 
@@ -549,18 +564,33 @@ hipError_t rows_t(const ActArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The stream's weight loads are non-temporal where a launch reads the weights
+// once: one row tile, and experts, most of which have one (without
+// the hint and with it 67.7 and 59.5 us for the 5 experts of d = 4096, 129 and 116 for 32 tokens x 2 of 8, 57.6 and
+// 49.6 for one layer of 8192 -> 28672 gated; one layer of 4096 -> 14336 gated,
+// out of the last-level cache, 22.1 and 21.7).  Two row tiles find each
+// other's weights in the caches: 29.0 us, with the hint 31.7.
+template <bool GATED, bool EX, int NS, int PW>
+hipError_t stream_e(const ActArgs& a, hipStream_t st) {
+  constexpr int SGB = GATED ? 1 : 2;
+  if constexpr (!EX) {
+    if (a.M > kRowsTile) return stream_t<NS, PW, SGB, GATED, EX, 3, false>(a, st);
+  }
+  return stream_t<NS, PW, SGB, GATED, EX, 3, true>(a, st);
+}
+
 // The stream from d = 2048 on: below, an item is over before a round trip
 // (64 experts of d = 1408, 24 tokens: 20 us against the rows kernel's 15.5;
-// d = 2048 equal; 5 experts of d = 4096: 60 against 71; one layer of d =
+// d = 2048 equal; 5 experts of d = 4096: 54 against 71; one layer of d =
 // 14336, 8 tokens: 12.3 against 19.4), and up to 16384, whose codes a wave
 // still holds in registers.
 template <bool GATED, bool EX>
 hipError_t rows_e(const ActArgs& a, hipStream_t st) {
   constexpr int SGB = GATED ? 1 : 2, RGB = GATED ? 2 : 4;
-  if (a.Kb >= 1024 && a.Kb <= 2048) return stream_t<4, 4, SGB, GATED, EX, 3>(a, st);
+  if (a.Kb >= 1024 && a.Kb <= 2048) return stream_e<GATED, EX, 4, 4>(a, st);
   // (ranks above 128 leave no room for 8 waves' rings)
   if (a.Kb > 2048 && a.Kb <= 8192 && stream_lds<8, SGB, GATED, 3>(a) <= 160 * 1024)
-    return stream_t<8, 8, SGB, GATED, EX, 3>(a, st);
+    return stream_e<GATED, EX, 8, 8>(a, st);
   return rows_t<RGB, GATED, EX, 2>(a, st);
 }
 

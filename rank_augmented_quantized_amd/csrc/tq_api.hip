@@ -1182,12 +1182,13 @@ struct ActWs {
 };
 // Experts with at most this many rows on average take the rows product, whose
 // prologue leaves nibble-packed codes and partials of T (both launches, rows
-// against tiles: 8 experts, 4096 -> 14336 gated, 4 rows each 98 and 119 us, 8
-// rows 129 and 132, 12 rows 135 and 131; 64 experts, 2048 -> 1024 gated, 8 rows
-// 44 and 48, 16 rows 54 and 50).  One layer takes it up to kSmallN rows as
+// against tiles: 8 experts, 4096 -> 14336 gated, 4 rows each 83 and 119 us, 8
+// rows 116 and 132, 12 rows 121 and 132, 16 rows 132 and 132; 128 experts of
+// 2048 -> 768 gated, 12.5 rows 67 and 68; 64 experts, 2048 -> 1024 gated, 8 rows
+// 43 and 48, 16 rows 55 and 50).  One layer takes it up to kSmallN rows as
 // tq_linear does (32 rows, 4096 -> 4096: 14.7 against 25.4 us; 4096 -> 14336
 // gated: 28 against 27).
-constexpr int64_t kSmallExpertRows = 8;
+constexpr int64_t kSmallExpertRows = 12;
 // Most k-chunk partials of T that the rows product sums.
 constexpr int kMaxTChunks = 16;
 
